@@ -401,6 +401,103 @@ moe_status_t moe_q6_k_pack(const void* blocks, int64_t n_mats, int64_t rows, int
  * with n > 0.  No counterpart on the pages (see MOE_WFMT_BF16_F16DOWN). */
 moe_status_t moe_bf16_to_f16(const void* src, int64_t n, void* dst, void* stream);
 
+/* ------------------------------------------------- the experts' operators
+ * The parts of the layer's expert FFNs as operators of their own, for callers
+ * that train the layer or put other work between its products: matrix
+ * products grouped by expert with their two gradients, SwiGLU rows with their
+ * gradient, and the same path with 8-bit activations and weights.  The pages
+ * have no counterpart (they describe inference through the fused layer only).
+ * They need no plan and keep no state between calls, so calls may run side by
+ * side on several streams; each runs on the current device, where all of its
+ * pointers must live (INVALID_ARG otherwise).  A first call on a device may
+ * load the library's module and raises the kernels' shared-memory limits:
+ * make it before a stream capture.  Outputs must not overlap inputs, except
+ * where it says so. */
+typedef enum moe_dtype {
+    MOE_DTYPE_BF16 = 0,
+    MOE_DTYPE_F16 = 1,
+    MOE_DTYPE_F32 = 2,
+    MOE_DTYPE_I8 = 3      /* signed 8-bit codes */
+} moe_dtype_t;
+
+/* A product grouped by expert.  Rows offsets[e] .. offsets[e+1] - 1 of the
+ * row-major sides belong to expert e, as moe_route sorts them (the offsets of
+ * moe_routing_t); an expert may have none.  Rows before offsets[0] and from
+ * offsets[E] on belong to nobody: they are not written, and what they hold
+ * reaches no result.  The table is read on the device; one that does not
+ * ascend from >= 0 to <= rows makes the call write nothing and sets the flag
+ * that moe_grouped_status reads. */
+typedef struct moe_grouped {
+    int64_t rows;            /* rows of x and y, 0 .. 2^30 */
+    int32_t n_experts;       /* E, 1 .. 1024 */
+    int32_t d_in;            /* multiple of 8 (of 16 in 8 bits, and <= 131056: the int32 sums stay exact) */
+    int32_t d_out;           /* multiple of 8 */
+    int32_t dtype;           /* moe_dtype_t of x, w and dy: BF16 or F16 (I8 in 8 bits) */
+    int32_t out_dtype;       /* of the result: dtype or F32 (in 8 bits BF16, F16 or F32) */
+    int32_t accumulate;      /* moe_grouped_wgrad with F32 only: 1 adds to dw, 0 overwrites it */
+    const int32_t* offsets;  /* device, [E+1] */
+    int64_t x_stride;        /* elements from row to row of x / dx: >= d_in, a multiple of 8 (16 in 8 bits) */
+    int64_t y_stride;        /* elements from row to row of y / dy: >= d_out, a multiple of 8 */
+} moe_grouped_t;
+
+/* y[r] = W[e] x[r] for the rows r of each expert e: x [rows][d_in],
+ * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once.  Every
+ * row's result depends on its own x and its expert's weights alone. */
+moe_status_t moe_grouped_gemm(const moe_grouped_t* g, const void* x, const void* w, void* y,
+                              void* stream);
+
+/* The gradient of its input: dx[r] = W[e]^T dy[r], dx of out_dtype. */
+moe_status_t moe_grouped_dgrad(const moe_grouped_t* g, const void* dy, const void* w, void* dx,
+                               void* stream);
+
+/* The gradient of its weights: dw[e] = sum over e's rows of dy[r] x[r]^T,
+ * dw [E][d_out][d_in] of out_dtype.  An expert without rows gets zeros (with
+ * accumulate: is left as it was).  The order of the sums is fixed. */
+moe_status_t moe_grouped_wgrad(const moe_grouped_t* g, const void* dy, const void* x, void* dw,
+                               void* stream);
+
+/* Rows of x [rows][cols] (BF16 or F16) as 8-bit codes and a scale for each
+ * row: s = max |x| / 127 and q = x / s rounded to the nearest integer (ties to
+ * even), at most 127 in absolute value.  A row of zeros gets s = 0; one that
+ * holds an infinity or a NaN gets s = NaN and codes 0, so that its products are
+ * NaN.  cols and the strides are multiples of 8.  Weights are rounded by the
+ * same call: the rows of w [E * d_out][d_in] give a scale for each output
+ * channel. */
+moe_status_t moe_i8_quantize(int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                             int64_t x_stride, void* q, int64_t q_stride, float* scale, void* stream);
+
+/* The grouped product of 8-bit codes: y[r][n] = x_scale[r] w_scale[e][n] *
+ * sum_k xq[r][k] wq[e][n][k], the sum exact in int32; xq [rows][d_in],
+ * x_scale [rows], wq [E][d_out][d_in], w_scale [E][d_out]. */
+moe_status_t moe_i8_grouped_gemm(const moe_grouped_t* g, const void* xq, const float* x_scale,
+                                 const void* wq, const float* w_scale, void* y, void* stream);
+
+/* h = silu(gate) * up by element, in fp32, rounded once: gate, up [rows][cols]
+ * with one row stride (halves of one [rows][2 cols] product, for instance), h
+ * of the same type.  cols and the strides are multiples of 8.  h may be gate or
+ * up itself, with their stride. */
+moe_status_t moe_swiglu(int64_t rows, int32_t cols, int32_t dtype, const void* gate, const void* up,
+                        int64_t in_stride, void* h, int64_t h_stride, void* stream);
+
+/* Its gradients: with s = sigmoid(gate), dgate = dh up s (1 + gate (1 - s)) and
+ * dup = dh gate s.  dgate and dup have one row stride; they may be gate and up
+ * themselves, with their stride. */
+moe_status_t moe_swiglu_grad(int64_t rows, int32_t cols, int32_t dtype, const void* dh,
+                             int64_t dh_stride, const void* gate, const void* up, int64_t in_stride,
+                             void* dgate, void* dup, int64_t grad_stride, void* stream);
+
+/* moe_swiglu and moe_i8_quantize in one pass: the codes and scales of silu(gate)
+ * * up as it stands in fp32, without the rounding of h. */
+moe_status_t moe_swiglu_i8(int64_t rows, int32_t cols, int32_t dtype, const void* gate,
+                           const void* up, int64_t in_stride, void* q, int64_t q_stride, float* scale,
+                           void* stream);
+
+/* Read and clear the sticky error word of the experts' operators on the
+ * current device (synchronises the device): OK, DEVICE_FLAG (an offsets table
+ * that was not sound; that call wrote nothing) or TIMEOUT (a bounded wait ran
+ * out; that call's output is incomplete). */
+moe_status_t moe_grouped_status(void);
+
 /* Static description of a status code (never NULL).  No counterpart on the
  * pages. */
 const char* moe_status_string(moe_status_t status);

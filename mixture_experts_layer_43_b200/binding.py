@@ -35,6 +35,11 @@ MOE_REGIME_DECODE = 1
 MOE_REGIME_PREFILL = 2
 MOE_DECODE_MAX_T = 8
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+MOE_DTYPE_I8 = 3
+
 
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
@@ -63,6 +68,13 @@ class moe_routing_t(ctypes.Structure):
     _fields_ = [("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
                 ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("slot_pair", ctypes.c_void_p)]
+
+
+class moe_grouped_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_experts", ctypes.c_int32), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -126,6 +138,22 @@ def lib() -> ctypes.CDLL:
     L.moe_q6_k_pack.restype = S
     L.moe_bf16_to_f16.argtypes = [P, I64, P, P]
     L.moe_bf16_to_f16.restype = S
+    G = ctypes.POINTER(moe_grouped_t)
+    for name in ("moe_grouped_gemm", "moe_grouped_dgrad", "moe_grouped_wgrad"):
+        getattr(L, name).argtypes = [G, P, P, P, P]
+        getattr(L, name).restype = S
+    L.moe_i8_grouped_gemm.argtypes = [G, P, P, P, P, P, P]
+    L.moe_i8_grouped_gemm.restype = S
+    L.moe_i8_quantize.argtypes = [I64, I32, I32, P, I64, P, I64, P, P]
+    L.moe_i8_quantize.restype = S
+    L.moe_swiglu.argtypes = [I64, I32, I32, P, P, I64, P, I64, P]
+    L.moe_swiglu.restype = S
+    L.moe_swiglu_grad.argtypes = [I64, I32, I32, P, I64, P, P, I64, P, P, I64, P]
+    L.moe_swiglu_grad.restype = S
+    L.moe_swiglu_i8.argtypes = [I64, I32, I32, P, P, I64, P, I64, P, P]
+    L.moe_swiglu_i8.restype = S
+    L.moe_grouped_status.argtypes = []
+    L.moe_grouped_status.restype = S
     _lib = L
     return L
 
@@ -254,3 +282,54 @@ def moe_q6_k_pack(blocks: int, n_mats: int, rows: int, k: int, codes: int, scale
 
 def moe_bf16_to_f16(src: int, n: int, dst: int, stream: int = 0) -> None:
     _check(lib().moe_bf16_to_f16(src, n, dst, stream), "moe_bf16_to_f16")
+
+
+def moe_grouped_gemm(g: moe_grouped_t, x: int, w: int, y: int, stream: int = 0) -> None:
+    """y[r] = w[e] x[r] for the rows of each expert."""
+    _check(lib().moe_grouped_gemm(ctypes.byref(g), x, w, y, stream), "moe_grouped_gemm")
+
+
+def moe_grouped_dgrad(g: moe_grouped_t, dy: int, w: int, dx: int, stream: int = 0) -> None:
+    """dx[r] = w[e]^T dy[r]: the gradient of moe_grouped_gemm's input."""
+    _check(lib().moe_grouped_dgrad(ctypes.byref(g), dy, w, dx, stream), "moe_grouped_dgrad")
+
+
+def moe_grouped_wgrad(g: moe_grouped_t, dy: int, x: int, dw: int, stream: int = 0) -> None:
+    """dw[e] (+)= sum of dy[r] x[r]^T: the gradient of moe_grouped_gemm's weights."""
+    _check(lib().moe_grouped_wgrad(ctypes.byref(g), dy, x, dw, stream), "moe_grouped_wgrad")
+
+
+def moe_i8_quantize(rows: int, cols: int, dtype: int, x: int, x_stride: int, q: int, q_stride: int,
+                    scale: int, stream: int = 0) -> None:
+    _check(lib().moe_i8_quantize(rows, cols, dtype, x, x_stride, q, q_stride, scale, stream),
+           "moe_i8_quantize")
+
+
+def moe_i8_grouped_gemm(g: moe_grouped_t, xq: int, x_scale: int, wq: int, w_scale: int, y: int,
+                        stream: int = 0) -> None:
+    _check(lib().moe_i8_grouped_gemm(ctypes.byref(g), xq, x_scale, wq, w_scale, y, stream),
+           "moe_i8_grouped_gemm")
+
+
+def moe_swiglu(rows: int, cols: int, dtype: int, gate: int, up: int, in_stride: int, h: int,
+               h_stride: int, stream: int = 0) -> None:
+    _check(lib().moe_swiglu(rows, cols, dtype, gate, up, in_stride, h, h_stride, stream),
+           "moe_swiglu")
+
+
+def moe_swiglu_grad(rows: int, cols: int, dtype: int, dh: int, dh_stride: int, gate: int, up: int,
+                    in_stride: int, dgate: int, dup: int, grad_stride: int, stream: int = 0) -> None:
+    _check(lib().moe_swiglu_grad(rows, cols, dtype, dh, dh_stride, gate, up, in_stride, dgate, dup,
+                                 grad_stride, stream), "moe_swiglu_grad")
+
+
+def moe_swiglu_i8(rows: int, cols: int, dtype: int, gate: int, up: int, in_stride: int, q: int,
+                  q_stride: int, scale: int, stream: int = 0) -> None:
+    _check(lib().moe_swiglu_i8(rows, cols, dtype, gate, up, in_stride, q, q_stride, scale, stream),
+           "moe_swiglu_i8")
+
+
+def moe_grouped_status() -> int:
+    """Raw status of the experts' operators' sticky error word on the current
+    device (not raised)."""
+    return lib().moe_grouped_status()

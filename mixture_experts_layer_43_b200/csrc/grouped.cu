@@ -1,0 +1,701 @@
+// grouped.cu -- matrix products grouped by expert on the tcgen05 tensor cores.
+//
+// Rows o_e .. o_{e+1} - 1 of the row-major sides belong to expert e, whose
+// weights are W[e] [d_out][d_in].  Three products and one in 8 bits:
+//   gemm   y[r][n]  = sum_k x[r][k] W[e][n][k]
+//   dgrad  dx[r][k] = sum_n dy[r][n] W[e][n][k]
+//   wgrad  dW[e][n][k] = sum over e's rows of dy[r][n] x[r][k]
+//   gemm of 8-bit codes: the sum in int32, times a scale for each row and one
+//   for each output channel
+//
+// Tiles.  A CTA pair (tcgen05.mma.cta_group::2) computes a 256 x <= 256 tile.
+// In gemm and dgrad the weights are the 256-row M side and the expert's rows
+// the N side: N of an MMA is a run-time field of its instruction descriptor,
+// so a ragged segment costs its rows rounded up to 32, not to a 128- or
+// 256-row tile.  An expert's rows are split evenly into ceil(n / 256) chunks.
+// Rows of a neighbouring expert that a chunk's loads touch only reach MMA
+// columns that are not stored.  In wgrad M and N are d_out and d_in (both
+// operands are "MN-major": the reduction runs over the rows of shared memory)
+// and the rows are the reduction; the rows past the segment's end in its last
+// step are overwritten with zeros in shared memory before the MMA reads them,
+// since they hold another expert's values (and 0 * NaN would not vanish).
+//
+// Roles of a CTA: warp 0 loads by TMA into a ring of six 32 KB stages, warp 1
+// of the pair's first CTA issues the MMAs, four warps drain the accumulator
+// (two of 256 TMEM columns each, so that they overlap the next tile's MMAs);
+// wgrad has one more warp that zeroes the rows of the last step.
+#include <atomic>
+
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "grouped.cuh"
+#include "umma_pair.cuh"
+
+namespace moe {
+
+static __device__ uint32_t g_grouped_err;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kTile = 256;                        // tile rows (M), and the most columns (N)
+constexpr int kHalf = 128;                        // rows of the tile one CTA holds
+constexpr int kKBytes = 128;                      // k-step: 64 16-bit or 128 8-bit elements
+constexpr int kStageHalf = kHalf * kKBytes;       // 16 KB, of A and of B
+constexpr int kStage = 2 * kStageHalf;
+constexpr int kStages = 6;
+constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
+constexpr int kEpiBox = 4096;                     // wgrad: one 32-row x 128-byte store box
+constexpr int kEpiBytes = 4 * 2 * kEpiBox;        // ... two for each epilogue warp
+
+struct TcArgs {
+    CUtensorMap tmA, tmB, tmD;
+    const int32_t* offsets;
+    void* out;
+    const float* a_scale;
+    const float* w_scale;
+    int64_t out_stride;
+    int64_t rows;
+    int E;
+    int M, N;              // M: output features.  N: wgrad's columns (d_in)
+    int nk;                // k-steps of gemm and dgrad
+    int out_dtype, accumulate;
+    uint32_t idesc;        // without the N field
+};
+
+// Descriptor of an MN-major 16-bit tile as TMA wrote it with the 128-byte
+// swizzle: one box is 64 MN elements (128 B) x 64 k rows; 8-row groups of k
+// are 1024 B apart (stride byte offset) and the next 64 MN elements one box
+// (8 KB) further (leading byte offset).
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+template <bool I8>
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    if constexpr (I8)
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+    else
+        umma_bf16_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
+}
+
+// TMA loads that complete on the mbarrier of either CTA of the pair (`mbar`
+// is a shared::cluster address).  No multicast.
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, uint32_t mbar,
+                                            int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(mbar), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, uint32_t mbar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+// The same into this CTA with its own mbarrier.
+__device__ __forceinline__ void tma_own_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
+                                           int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0,
+                                             int32_t c1, int32_t c2, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+                     " [%0, {%2, %3, %4}], [%1];"
+                     ::"l"(map), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
+                     " [%0, {%2, %3, %4}], [%1];"
+                     ::"l"(map), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Bounded wait whose acquire covers the other CTA of the pair.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if (t0 == 0) t0 = globaltimer_ns();
+        else if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
+
+// A tile of the product.  gemm and dgrad: feature rows m0.., token rows
+// row0 .. row0 + valid - 1 as columns.  wgrad: weight rows m0.., columns n0..,
+// reduction over row0 .. row0 + valid - 1.
+struct Tile {
+    int e, m0, n0, row0, valid;
+    int cols;        // MMA N: valid columns rounded up to 32
+    int nk;
+};
+
+// Walks the tile numbers first, first + step, ...: expert-major; in gemm and
+// dgrad the chunks of an expert's rows vary fastest, so that the CTAs that run
+// together share the weight rows (which come from HBM once) and the chunks.
+template <int OP>
+struct TileWalk {
+    const TcArgs& a;
+    const int* off;        // in shared memory (wgrad: the caller's table)
+    const int* base;       // gemm, dgrad: chunks of the experts before e
+    int mt, nt;
+    int64_t t, total;
+    int step, e = 0;
+
+    __device__ TileWalk(const TcArgs& args, const int* s_off, const int* s_base, int first, int n)
+        : a(args), off(s_off), base(s_base), t(first), step(n) {
+        mt = (a.M + kTile - 1) / kTile;
+        nt = OP == kOpWgrad ? (a.N + kTile - 1) / kTile : 0;
+        total = OP == kOpWgrad ? static_cast<int64_t>(a.E) * mt * nt
+                               : static_cast<int64_t>(base[a.E]) * mt;
+    }
+    __device__ bool next(Tile& g) {
+        if (t >= total) return false;
+        if constexpr (OP == kOpWgrad) {
+            const int per = mt * nt;
+            g.e = static_cast<int>(t / per);
+            const int r = static_cast<int>(t - static_cast<int64_t>(g.e) * per);
+            g.m0 = (r / nt) * kTile;
+            g.n0 = (r % nt) * kTile;
+            g.row0 = off[g.e];
+            g.valid = off[g.e + 1] - g.row0;
+            g.cols = (min(kTile, a.N - g.n0) + 31) & ~31;
+            g.nk = (g.valid + 63) / 64;
+        } else {
+            while (static_cast<int64_t>(base[e + 1]) * mt <= t) ++e;
+            const int n = off[e + 1] - off[e];
+            const int c = base[e + 1] - base[e];
+            const int64_t r = t - static_cast<int64_t>(base[e]) * mt;
+            const int per = ((n + c - 1) / c + 31) & ~31;
+            const int mi = static_cast<int>(r / c), ci = static_cast<int>(r % c);
+            g.e = e;
+            g.m0 = mi * kTile;
+            g.n0 = 0;
+            g.row0 = off[e] + ci * per;
+            g.valid = min(per, n - ci * per);
+            g.cols = (g.valid + 31) & ~31;
+            g.nk = a.nk;
+        }
+        t += step;
+        return true;
+    }
+};
+
+// Offsets into shared memory, checked; and the running count of row chunks.
+// Returns false (for every thread of the block) if the table is not sound.
+template <int OP>
+__device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base) {
+    bool bad = false;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+        const int v = a.offsets[e];
+        const int next = e < a.E ? a.offsets[e + 1] : v;
+        bad |= v < 0 || v > a.rows || next < v;
+        if (OP != kOpWgrad) s_off[e] = v;
+    }
+    bad = __syncthreads_or(bad);
+    if (!bad && OP != kOpWgrad && threadIdx.x < 32) {
+        int sum = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + static_cast<int>(threadIdx.x);
+            int c = e < a.E ? (s_off[e + 1] - s_off[e] + kTile - 1) / kTile : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, c, d);
+                if (static_cast<int>(threadIdx.x) >= d) c += o;
+            }
+            if (e < a.E) s_base[e + 1] = sum + c;
+            sum += __shfl_sync(0xffffffffu, c, 31);
+        }
+        if (threadIdx.x == 0) s_base[0] = 0;
+    }
+    return !bad;
+}
+
+template <int OP>
+constexpr int tc_threads() { return OP == kOpWgrad ? 224 : 192; }
+
+template <int OP, bool I8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads<OP>(), 1)
+grouped_tc_kernel(const __grid_constant__ TcArgs a) {
+    constexpr int kElem = I8 ? 1 : 2;
+    constexpr int kBK = kKBytes / kElem;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* epi = ring + kStages * kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + (OP == kOpWgrad ? kEpiBytes : 0));
+    uint64_t* empty = full + kStages;
+    uint64_t* landed = empty + kStages;              // wgrad: this CTA's loads
+    uint64_t* tfull = landed + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
+    int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+    int* s_off = s_abort + 1;
+    int* s_base = s_off + a.E + 1;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int unit = static_cast<int>(blockIdx.x) / 2, n_units = static_cast<int>(gridDim.x) / 2;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], OP == kOpWgrad ? 2 : 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&landed[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 8); }
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    const bool sound = load_offsets<OP>(a, s_off, s_base);   // the same in both CTAs
+    if (!sound) {
+        if (tid == 0) atomicOr(&g_grouped_err, kErrBadId);
+        return;
+    }
+    if (warp == 1) tmem_alloc_pair(s_tmem, 512);
+    tc_fence_before();
+    cluster_sync_all();       // the peer's barriers are initialised before any signal
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    volatile int* abort_flag = s_abort;
+    auto fail = [&]() { atomicOr(&g_grouped_err, kErrTimeout); *abort_flag = 1; };
+    TileWalk<OP> walk(a, OP == kOpWgrad ? a.offsets : s_off, s_base, unit, n_units);
+    Tile g;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tensormap(&a.tmA);
+            prefetch_tensormap(&a.tmB);
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && !*abort_flag && walk.next(g)) {
+                const int half = g.cols / 2;                  // N rows (columns) of this CTA
+                const int m0 = g.m0 + kHalf * rank;
+                // boxes of the N side: 32 token rows, or (wgrad) 64 columns
+                const int nb = OP == kOpWgrad ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
+                const uint32_t bytes = kStageHalf + nb * (OP == kOpWgrad ? 8192u : kBoxRows * kKBytes);
+                for (int kb = 0; kb < g.nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= static_cast<uint32_t>(kStages) &&
+                        !mbar_wait_bounded(&empty[s], ((it / kStages) - 1) & 1)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) { ok = false; break; }
+                    uint8_t* A = ring + s * kStage;
+                    uint8_t* B = A + kStageHalf;
+                    if constexpr (OP == kOpWgrad) {
+                        mbar_arrive_expect_tx(&landed[s], bytes);
+                        const int r = g.row0 + kb * 64;
+                        tma_own_2d(A, &a.tmA, &landed[s], m0, r);
+                        tma_own_2d(A + 8192, &a.tmA, &landed[s], m0 + 64, r);
+                        for (int j = 0; j < nb; ++j)
+                            tma_own_2d(B + j * 8192, &a.tmB, &landed[s], g.n0 + half * rank + 64 * j, r);
+                    } else {
+                        // the loads of both CTAs complete on the first one's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                        const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                        if constexpr (OP == kOpGemm) {
+                            tma_pair_3d(A, &a.tmA, bar, kb * kBK, m0, g.e);
+                        } else {
+                            tma_pair_3d(A, &a.tmA, bar, m0, kb * kBK, g.e);
+                            tma_pair_3d(A + 8192, &a.tmA, bar, m0 + 64, kb * kBK, g.e);
+                        }
+                        for (int j = 0; j < nb; ++j)
+                            tma_pair_2d(B + j * kBoxRows * kKBytes, &a.tmB, bar, kb * kBK,
+                                        g.row0 + half * rank + kBoxRows * j);
+                    }
+                }
+            }
+            // every issued stage released by the MMAs: no commit arrives in
+            // this CTA's shared memory after it exits
+            const uint32_t first = it > static_cast<uint32_t>(kStages) ? it - kStages : 0u;
+            for (uint32_t q = first; q < it && ok; ++q)
+                if (!mbar_wait_bounded(&empty[q % kStages], (q / kStages) & 1)) {
+                    fail();
+                    break;
+                }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0;
+            int local = 0;
+            bool ok = true;
+            for (; ok && !*abort_flag && walk.next(g); ++local) {
+                const int b = local & 1;
+                if (local >= 2 && !mbar_wait_cluster(&tempty[b], ((local >> 1) - 1) & 1)) {
+                    fail();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem + b * kTile;
+                const uint32_t idesc = a.idesc | (static_cast<uint32_t>(g.cols >> 3) << 17);
+                for (int kb = 0; kb < g.nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (*abort_flag || !mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t A = smem_u32(ring + s * kStage);
+                    const uint32_t B = A + kStageHalf;
+                    if constexpr (OP == kOpWgrad) {
+                        const int steps = min(4, (g.valid - kb * 64 + 15) / 16);
+                        for (int kk = 0; kk < steps; ++kk)
+                            umma_pair<false>(d_tmem, umma_desc_mn_sw128(A + kk * 2048),
+                                             umma_desc_mn_sw128(B + kk * 2048), idesc, (kb | kk) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t ad = OP == kOpGemm ? umma_desc_sw128(A + kk * 32)
+                                                              : umma_desc_mn_sw128(A + kk * 2048);
+                            umma_pair<I8>(d_tmem, ad, umma_desc_sw128(B + kk * 32), idesc,
+                                          (kb | kk) ? 1u : 0u);
+                        }
+                    }
+                    umma_commit_pair(&empty[s]);
+                }
+                if (ok) umma_commit_pair(&tfull[b]);
+            }
+        }
+    } else if (warp < 6) {
+        // ----------------------------------------------------- epilogue
+        const int q = warp & 3;                        // TMEM lane quarter of this warp
+        int local = 0, n_box = 0;
+        for (; walk.next(g); ++local) {
+            // every decision before the warp-collective tcgen05.ld is warp-uniform
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int b = local & 1;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tfull[b], (local >> 1) & 1));
+            if (!ok) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile;
+            const int f0 = g.m0 + kHalf * rank + q * 32;      // this warp's first feature
+            if constexpr (OP == kOpWgrad) {
+                // 32 rows x 128 bytes at a time through shared memory: each
+                // thread writes its row's 16-byte chunks XOR-swizzled (as the
+                // store's map reads them), then one TMA store per box
+                const int per = a.out_dtype == MOE_DTYPE_F32 ? 32 : 64;
+                const uint32_t stg = smem_u32(epi) + (warp - 2) * 2 * kEpiBox;
+                const uint32_t row = stg + lane * 128;
+                for (int c = 0; c < g.cols && f0 < a.M && (g.nk || !a.accumulate); c += per, ++n_box) {
+                    uint32_t v[32], p[32];
+                    if (g.nk) tmem_ld32(taddr + c, v);
+                    tmem_ld_wait();
+                    if (per == 64) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
+                            p[i] = a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+                        }
+                        if (g.nk && c + 32 < g.cols) tmem_ld32(taddr + c + 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
+                            p[16 + i] = a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) p[i] = v[i];
+                    }
+                    if (g.nk == 0) {               // an expert without rows
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) p[i] = 0u;
+                    }
+                    // the box of two rounds ago has left shared memory
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t buf = (n_box & 1) * kEpiBox;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(row + buf + ((j ^ (lane & 7)) * 16)), "r"(p[4 * j]),
+                                       "r"(p[4 * j + 1]), "r"(p[4 * j + 2]), "r"(p[4 * j + 3]) : "memory");
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (g.n0 + c < a.N) tma_store_3d(&a.tmD, stg + buf, g.n0 + c, f0, g.e, a.accumulate != 0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                }
+            } else {
+                const int f = f0 + lane;
+                const float ws = I8 && f < a.M ? a.w_scale[static_cast<int64_t>(g.e) * a.M + f] : 1.f;
+#pragma unroll 1
+                for (int c = 0; c < g.valid; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(taddr + c, v);
+                    tmem_ld_wait();
+                    const int64_t r0 = static_cast<int64_t>(g.row0) + c;
+                    if constexpr (I8) {
+                        const float as = c + lane < g.valid ? a.a_scale[r0 + lane] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(static_cast<float>(static_cast<int>(v[i])) *
+                                                   __shfl_sync(0xffffffffu, as, i) * ws);
+                    }
+                    if (a.out_dtype == MOE_DTYPE_F32) {
+                        float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < g.valid && f < a.M) o[i * a.out_stride] = __uint_as_float(v[i]);
+                    } else {
+                        // neighbouring lanes (features) trade columns, so that
+                        // each stores two features of one token: 4 bytes
+                        const int odd = lane & 1;
+                        uint16_t* o = static_cast<uint16_t*>(a.out) + (r0 + odd) * a.out_stride + (f & ~1);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                            const float lo = __uint_as_float(odd ? got : v[i]);
+                            const float hi = __uint_as_float(odd ? v[i + 1] : got);
+                            if (c + i + odd < g.valid && f < a.M)
+                                *reinterpret_cast<uint32_t*>(o + i * a.out_stride) =
+                                    a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));
+        }
+        if (OP == kOpWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else {
+        // wgrad: hands each stage to the MMA warp once this CTA's loads have
+        // landed, with the rows past the segment's end zeroed
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+            for (int kb = 0; kb < g.nk; ++kb, ++it) {
+                const int s = it % kStages;
+                ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(&landed[s], (it / kStages) & 1));
+                if (!ok) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                const int left = g.valid - kb * 64;
+                const int pad = left < 64 ? (-left & 15) : 0;      // rows left .. left + pad - 1
+                if (pad) {
+                    const uint32_t base = smem_u32(ring + s * kStage) + left * 128;
+                    for (int j = lane; j < pad * 8 * 4; j += 32) {  // four boxes of 64 columns
+                        const uint32_t at = base + (j / (pad * 8)) * 8192 + (j % (pad * 8)) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();          // no signal into a CTA that has left
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int OP>
+size_t tc_smem_bytes(int E) {
+    return 1024 + kStages * kStage + (3 * kStages + 4) * 8 + 8 +
+           (OP == kOpWgrad ? kEpiBytes : 2 * (static_cast<size_t>(E) + 1) * 4);
+}
+
+// ================================================================= host ===
+struct DeviceInfo {
+    std::atomic<int> pairs{0};             // CTA pairs the device keeps resident; 0: not asked yet
+};
+DeviceInfo g_info[kMaxDevices];
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cached.store(fn, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+}
+
+// dims and box of up to three dimensions (innermost first); pitch in bytes.
+bool tile_map(CUtensorMap* m, int elem, const void* base, int nd, const uint64_t* dims,
+              const uint64_t* pitch, const uint32_t* box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return false;
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUtensorMapDataType t = elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                : elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return enc(m, t, nd, const_cast<void*>(base), dims, pitch, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rows_map(CUtensorMap* m, int elem, const void* base, int64_t cols, int64_t rows, int64_t stride,
+              uint32_t box_cols, uint32_t box_rows) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+    const uint64_t pitch[1] = {static_cast<uint64_t>(stride) * elem};
+    const uint32_t box[2] = {box_cols, box_rows};
+    return tile_map(m, elem, base, 2, dims, pitch, box);
+}
+
+bool stack_map(CUtensorMap* m, int elem, const void* base, int64_t cols, int64_t rows, int64_t n,
+               uint32_t box_cols, uint32_t box_rows) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(n)};
+    const uint64_t pitch[2] = {static_cast<uint64_t>(cols) * elem, static_cast<uint64_t>(cols) * rows * elem};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return tile_map(m, elem, base, 3, dims, pitch, box);
+}
+
+// Once per device: raise the kernels' shared-memory limit and ask how many
+// pairs fit.
+template <int OP, bool I8>
+bool prepare_kernel(int* pairs) {
+    auto* k = grouped_tc_kernel<OP, I8>;
+    const int smem = static_cast<int>(tc_smem_bytes<OP>(kMaxExperts));
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(tc_threads<OP>());
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return false;
+    *pairs = *pairs == 0 || n < *pairs ? n : *pairs;
+    return true;
+}
+
+int device_pairs() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = g_info[dev].pairs.load(std::memory_order_acquire);
+    if (n) return n;
+    if (!prepare_kernel<kOpGemm, false>(&n) || !prepare_kernel<kOpGemm, true>(&n) ||
+        !prepare_kernel<kOpDgrad, false>(&n) || !prepare_kernel<kOpWgrad, false>(&n)) {
+        cudaGetLastError();
+        return 0;
+    }
+    g_info[dev].pairs.store(n, std::memory_order_release);
+    return n;
+}
+
+template <int OP, bool I8>
+moe_status_t launch_tc(const TcArgs& a, int64_t tiles, cudaStream_t stream) {
+    const int pairs = device_pairs();
+    if (!pairs) return MOE_ERR_CUDA;
+    const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+    grouped_tc_kernel<OP, I8><<<grid, tc_threads<OP>(), tc_smem_bytes<OP>(a.E), stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t stream) {
+    const bool i8 = c.dtype == MOE_DTYPE_I8;
+    const int elem = i8 ? 1 : 2;
+    const int bk = kKBytes / elem;
+    if (c.rows == 0) {
+        if (op != kOpWgrad || c.accumulate) return MOE_OK;
+        const size_t n = static_cast<size_t>(c.E) * c.d_out * c.d_in * (c.out_dtype == MOE_DTYPE_F32 ? 4 : 2);
+        return cudaMemsetAsync(c.out, 0, n, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    TcArgs a;
+    memset(&a, 0, sizeof(a));
+    a.offsets = c.offsets;
+    a.out = c.out;
+    a.a_scale = c.a_scale;
+    a.w_scale = c.w_scale;
+    a.rows = c.rows;
+    a.E = c.E;
+    a.out_dtype = c.out_dtype;
+    a.accumulate = c.accumulate;
+    // D fp32 (int32), A and B bf16 (signed 8-bit; fp16 is 0), M 256 over the pair
+    a.idesc = (i8 ? 2u << 4 : 1u << 4) | (16u << 24);
+    if (c.dtype != MOE_DTYPE_F16) a.idesc |= (1u << 7) | (1u << 10);
+    bool ok = true;
+    int64_t tiles = 0;
+    const int64_t chunks = ceil_div(c.rows, kTile) + (c.rows < c.E ? c.rows : c.E);   // at most
+    if (op == kOpGemm) {
+        a.M = c.d_out;
+        a.nk = static_cast<int>(ceil_div(c.d_in, bk));
+        a.out_stride = c.y_stride;
+        ok &= stack_map(&a.tmA, elem, c.w, c.d_in, c.d_out, c.E, bk, kHalf);
+        ok &= rows_map(&a.tmB, elem, c.a, c.d_in, c.rows, c.x_stride, bk, kBoxRows);
+        tiles = chunks * ceil_div(a.M, kTile);
+    } else if (op == kOpDgrad) {
+        a.M = c.d_in;
+        a.nk = static_cast<int>(ceil_div(c.d_out, bk));
+        a.out_stride = c.x_stride;
+        a.idesc |= 1u << 15;                               // A MN-major
+        ok &= stack_map(&a.tmA, elem, c.w, c.d_in, c.d_out, c.E, 64, 64);
+        ok &= rows_map(&a.tmB, elem, c.a, c.d_out, c.rows, c.y_stride, bk, kBoxRows);
+        tiles = chunks * ceil_div(a.M, kTile);
+    } else {
+        a.M = c.d_out;
+        a.N = c.d_in;
+        a.idesc |= (1u << 15) | (1u << 16);                // A and B MN-major
+        ok &= rows_map(&a.tmA, elem, c.a, c.d_out, c.rows, c.y_stride, 64, 64);
+        ok &= rows_map(&a.tmB, elem, c.w, c.d_in, c.rows, c.x_stride, 64, 64);
+        const int oe = c.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+        ok &= stack_map(&a.tmD, oe, c.out, c.d_in, c.d_out, c.E, 128 / oe, 32);
+        tiles = static_cast<int64_t>(c.E) * ceil_div(a.M, kTile) * ceil_div(a.N, kTile);
+    }
+    if (!ok) return MOE_ERR_INVALID_ARG;
+    if (op == kOpGemm) return i8 ? launch_tc<kOpGemm, true>(a, tiles, stream)
+                                 : launch_tc<kOpGemm, false>(a, tiles, stream);
+    if (op == kOpDgrad) return launch_tc<kOpDgrad, false>(a, tiles, stream);
+    return launch_tc<kOpWgrad, false>(a, tiles, stream);
+}
+
+moe_status_t grouped_status_read() {
+    uint32_t v = 0;
+    const uint32_t zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(&v, g_grouped_err, 4) != cudaSuccess) return MOE_ERR_CUDA;
+    if (v && cudaMemcpyToSymbol(g_grouped_err, &zero, 4) != cudaSuccess) return MOE_ERR_CUDA;
+    if (v & kErrTimeout) return MOE_ERR_TIMEOUT;
+    return v ? MOE_ERR_DEVICE_FLAG : MOE_OK;
+}
+
+}  // namespace moe
