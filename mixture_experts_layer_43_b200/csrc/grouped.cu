@@ -14,7 +14,7 @@
 // so a ragged segment costs its rows rounded up to 32, not to a 128- or
 // 256-row tile.  An expert's rows are split evenly into ceil(n / 256) chunks.
 // Rows of a neighbouring expert that a chunk's loads touch only reach MMA
-// columns that are not stored.  In wgrad M and N are d_out and d_in (both
+// columns that are not stored.  In wgrad M and N are d_in and d_out (both
 // operands are "MN-major": the reduction runs over the rows of shared memory)
 // and the rows are the reduction; the rows past the segment's end in its last
 // step are overwritten with zeros in shared memory before the MMA reads them,
@@ -46,11 +46,12 @@ constexpr int kStageHalf = kHalf * kKBytes;       // 16 KB, of A and of B
 constexpr int kStage = 2 * kStageHalf;
 constexpr int kStages = 6;
 constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
-constexpr int kEpiBox = 4096;                     // wgrad: one 32-row x 128-byte store box
-constexpr int kEpiBytes = 4 * 2 * kEpiBox;        // ... two for each epilogue warp
+constexpr int kEpiWarps = 8;                      // two for each quarter of the TMEM lanes
+constexpr int kEpiBytes = kEpiWarps * 128;        // 8 bits: 32 scales for each
 
 struct TcArgs {
-    CUtensorMap tmA, tmB, tmD;
+    CUtensorMap tmA, tmB;
+    CUtensorMap tmB128;        // gemm, dgrad: tmB's rows in boxes of 128
     const int32_t* offsets;
     void* out;
     const float* a_scale;
@@ -58,8 +59,9 @@ struct TcArgs {
     int64_t out_stride;
     int64_t rows;
     int E;
-    int M, N;              // M: output features.  N: wgrad's columns (d_in)
+    int M, N;              // M: output features (wgrad: d_in).  N: wgrad's columns (d_out)
     int nk;                // k-steps of gemm and dgrad
+    int m_block;           // gemm, dgrad: weight tiles of a block (see TileWalk)
     int out_dtype, accumulate;
     uint32_t idesc;        // without the N field
 };
@@ -93,56 +95,59 @@ __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint
 
 // TMA loads that complete on the mbarrier of either CTA of the pair (`mbar`
 // is a shared::cluster address).  No multicast.
-__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, uint32_t mbar,
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
                                             int32_t c0, int32_t c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(mbar), "r"(c0), "r"(c1) : "memory");
+        ::"r"(dst), "l"(map), "r"(mbar), "r"(c0), "r"(c1) : "memory");
 }
-__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, uint32_t mbar,
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
                                             int32_t c0, int32_t c1, int32_t c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2) : "memory");
-}
-// The same into this CTA with its own mbarrier.
-__device__ __forceinline__ void tma_own_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
-                                           int32_t c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1) : "memory");
-}
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0,
-                                             int32_t c1, int32_t c2, bool add) {
-    if (add)
-        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
-                     " [%0, {%2, %3, %4}], [%1];"
-                     ::"l"(map), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
-                     " [%0, {%2, %3, %4}], [%1];"
-                     ::"l"(map), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
+        ::"r"(dst), "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// Bounded wait whose acquire covers the other CTA of the pair.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-        if (ok) return true;
-        if (t0 == 0) t0 = globaltimer_ns();
-        else if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// The rest of a wait whose first poll failed: at most kWaitLimitNs, and over at
+// once when another wait of this CTA has run out.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_cluster(bar, parity)) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(&g_grouped_err, kErrTimeout);
+            return false;
+        }
     }
+    return true;
+}
+// Bounded wait whose acquire covers the other CTA of the pair; false once a wait
+// of this CTA has run out.  The loops below do not leave on that (a vote in each
+// step costs a sixth of the MMA warp's rate at small tiles): the waits that
+// follow return at once and every role runs to its end, loading and storing
+// nothing more.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return mbar_try_wait_cluster(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
 }
 
 // A tile of the product.  gemm and dgrad: feature rows m0.., token rows
@@ -154,14 +159,15 @@ struct Tile {
     int nk;
 };
 
-// Walks the tile numbers first, first + step, ...: expert-major; in gemm and
-// dgrad the chunks of an expert's rows vary fastest, so that the CTAs that run
-// together share the weight rows (which come from HBM once) and the chunks.
+// Walks the tile numbers first, first + step, ...: expert by expert; within an
+// expert of gemm and dgrad by blocks of m_block weight tiles, and within a block
+// by row chunks, so that the block's weights stay in L2 while the rows stream by
+// once for each block.
 template <int OP>
 struct TileWalk {
     const TcArgs& a;
     const int* off;        // in shared memory (wgrad: the caller's table)
-    const int* base;       // gemm, dgrad: chunks of the experts before e
+    const int* base;       // gemm, dgrad: row chunks of the experts before e
     int mt, nt;
     int64_t t, total;
     int step, e = 0;
@@ -179,21 +185,30 @@ struct TileWalk {
             const int per = mt * nt;
             g.e = static_cast<int>(t / per);
             const int r = static_cast<int>(t - static_cast<int64_t>(g.e) * per);
-            g.m0 = (r / nt) * kTile;
-            g.n0 = (r % nt) * kTile;
+            // the shorter side varies fastest: its operand is what L2 keeps
+            g.m0 = (mt < nt ? r % mt : r / nt) * kTile;
+            g.n0 = (mt < nt ? r / mt : r % nt) * kTile;
             g.row0 = off[g.e];
             g.valid = off[g.e + 1] - g.row0;
             g.cols = (min(kTile, a.N - g.n0) + 31) & ~31;
             g.nk = (g.valid + 63) / 64;
         } else {
-            while (static_cast<int64_t>(base[e + 1]) * mt <= t) ++e;
+            int hi = a.E;                       // the last expert whose tiles start at or before t
+            while (hi - e > 1) {
+                const int mid = (e + hi) >> 1;
+                if (static_cast<int64_t>(base[mid]) * mt <= t) e = mid; else hi = mid;
+            }
+            const int c0 = base[e], chunks = base[e + 1] - c0;
+            const int64_t r = t - static_cast<int64_t>(c0) * mt;
+            const int per_block = chunks * a.m_block;
+            const int block = static_cast<int>(r / per_block);
+            const int in_block = static_cast<int>(r - static_cast<int64_t>(block) * per_block);
+            const int mb = min(a.m_block, mt - block * a.m_block);
+            const int ci = in_block / mb;
             const int n = off[e + 1] - off[e];
-            const int c = base[e + 1] - base[e];
-            const int64_t r = t - static_cast<int64_t>(base[e]) * mt;
-            const int per = ((n + c - 1) / c + 31) & ~31;
-            const int mi = static_cast<int>(r / c), ci = static_cast<int>(r % c);
+            const int per = ((n + chunks - 1) / chunks + 31) & ~31;
             g.e = e;
-            g.m0 = mi * kTile;
+            g.m0 = (block * a.m_block + in_block % mb) * kTile;
             g.n0 = 0;
             g.row0 = off[e] + ci * per;
             g.valid = min(per, n - ci * per);
@@ -236,7 +251,33 @@ __device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base) {
 }
 
 template <int OP>
-constexpr int tc_threads() { return OP == kOpWgrad ? 224 : 192; }
+constexpr int tc_threads() { return (2 + kEpiWarps + (OP == kOpWgrad ? 1 : 0)) * 32; }
+
+// 32 columns (tokens) of this lane's feature as 16-bit values, `n` of them
+// stored: even and odd lanes trade half of their packed pairs of tokens, so
+// that each holds two features (4 bytes) of 16 tokens.
+__device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const uint32_t (&v)[32], int n, bool f16,
+                                            uint32_t lanes) {
+    const int odd = threadIdx.x & 1;
+    const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
+    out += odd * 2 * stride;
+    n -= odd * 2;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        uint32_t p[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float x = __uint_as_float(v[i + 2 * j]), y = __uint_as_float(v[i + 2 * j + 1]);
+            p[j] = f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+        }
+        // an even lane keeps tokens i, i + 1 and an odd one i + 2, i + 3, of both features
+        const uint32_t got = __shfl_xor_sync(lanes, odd ? p[0] : p[1], 1);
+        const uint32_t keep = odd ? p[1] : p[0];
+        if (i < n) *reinterpret_cast<uint32_t*>(out) = __byte_perm(keep, got, sel_lo);
+        if (i + 1 < n) *reinterpret_cast<uint32_t*>(out + stride) = __byte_perm(keep, got, sel_hi);
+        out += 4 * stride;
+    }
+}
 
 template <int OP, bool I8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads<OP>(), 1)
@@ -247,26 +288,29 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* epi = ring + kStages * kStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(epi + (OP == kOpWgrad ? kEpiBytes : 0));
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + kEpiBytes);
     uint64_t* empty = full + kStages;
-    uint64_t* landed = empty + kStages;              // wgrad: this CTA's loads
-    uint64_t* tfull = landed + kStages;
+    uint64_t* landed = empty + kStages;              // wgrad: this CTA's loads of a step to pad
+    uint64_t* padded = landed + kStages;             // ... and both CTAs' zeros written
+    uint64_t* tfull = padded + kStages;
     uint64_t* tempty = tfull + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
     int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
     int* s_off = s_abort + 1;
     int* s_base = s_off + a.E + 1;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);      // the same in every lane, and known to be
     const int rank = static_cast<int>(cluster_ctarank());
     const int unit = static_cast<int>(blockIdx.x) / 2, n_units = static_cast<int>(gridDim.x) / 2;
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], OP == kOpWgrad ? 2 : 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&landed[s], 1);
+            mbar_init(&padded[s], 2);
         }
-        for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 8); }
+        for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * kEpiWarps); }
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -279,245 +323,231 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     tc_fence_before();
     cluster_sync_all();       // the peer's barriers are initialised before any signal
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
+    const uint32_t ring_base = smem_u32(ring);
+    const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(full), 0), 0);   // the first CTA's full[0]
+    const uint32_t landed0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(landed), rank), 0);
     volatile int* abort_flag = s_abort;
-    auto fail = [&]() { atomicOr(&g_grouped_err, kErrTimeout); *abort_flag = 1; };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_cluster(bar, parity, abort_flag); };
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed);
+    const uint32_t padded_u = smem_u32(padded), tfull_u = smem_u32(tfull), tempty_u = smem_u32(tempty);
     TileWalk<OP> walk(a, OP == kOpWgrad ? a.offsets : s_off, s_base, unit, n_units);
     Tile g;
 
     if (warp == 0) {
         // ------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tensormap(&a.tmA);
             prefetch_tensormap(&a.tmB);
-            uint32_t it = 0;
-            bool ok = true;
-            while (ok && !*abort_flag && walk.next(g)) {
-                const int half = g.cols / 2;                  // N rows (columns) of this CTA
-                const int m0 = g.m0 + kHalf * rank;
-                // boxes of the N side: 32 token rows, or (wgrad) 64 columns
-                const int nb = OP == kOpWgrad ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
-                const uint32_t bytes = kStageHalf + nb * (OP == kOpWgrad ? 8192u : kBoxRows * kKBytes);
-                for (int kb = 0; kb < g.nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (it >= static_cast<uint32_t>(kStages) &&
-                        !mbar_wait_bounded(&empty[s], ((it / kStages) - 1) & 1)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (*abort_flag) { ok = false; break; }
-                    uint8_t* A = ring + s * kStage;
-                    uint8_t* B = A + kStageHalf;
+        }
+        __syncwarp();
+        int s = 0;
+        uint32_t phase = 1;                      // a ring that was never filled is free
+        int used = 0;                            // stages filled at least once
+        bool stop = false;
+        while (walk.next(g)) {
+            const int half = g.cols / 2;                  // N rows (columns) of this CTA
+            const int m0 = g.m0 + kHalf * rank;
+            // boxes of the N side: 64 columns (wgrad), or 32 token rows; more than
+            // 96 rows take one box of 128
+            const bool big = OP != kOpWgrad && half > 96;
+            const int nb = OP == kOpWgrad ? (half + 63) / 64 : big ? 4 : (half + kBoxRows - 1) / kBoxRows;
+            const uint32_t bytes = kStageHalf + nb * (OP == kOpWgrad ? 8192u : kBoxRows * kKBytes);
+            const int r0 = OP == kOpWgrad ? g.row0 : g.row0 + half * rank;
+            for (int kb = 0; kb < g.nk; ++kb) {
+                stop |= !wait(empty_u + s * 8, phase);
+                const uint32_t A = ring_base + s * kStage;
+                const uint32_t B = A + kStageHalf;
+                if (elect_one() && !stop) {
                     if constexpr (OP == kOpWgrad) {
-                        mbar_arrive_expect_tx(&landed[s], bytes);
-                        const int r = g.row0 + kb * 64;
-                        tma_own_2d(A, &a.tmA, &landed[s], m0, r);
-                        tma_own_2d(A + 8192, &a.tmA, &landed[s], m0 + 64, r);
-                        for (int j = 0; j < nb; ++j)
-                            tma_own_2d(B + j * 8192, &a.tmB, &landed[s], g.n0 + half * rank + 64 * j, r);
+                        // a last step that needs padding lands on this CTA's own
+                        // barrier, every other on the first CTA's
+                        const bool pad = kb == g.nk - 1 && (g.valid & 15);
+                        if (pad) mbar_arrive_expect_tx(&landed[s], bytes);
+                        if (rank == 0) {
+                            if (pad) mbar_arrive(&full[s]);
+                            else mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                        }
+                        const uint32_t bar = pad ? landed0 + s * 8 : full0 + s * 8;
+                        const int r = r0 + kb * 64;
+                        tma_pair_2d(A, &a.tmA, bar, m0, r);
+                        tma_pair_2d(A + 8192, &a.tmA, bar, m0 + 64, r);
+                        tma_pair_2d(B, &a.tmB, bar, g.n0 + half * rank, r);
+                        if (nb > 1) tma_pair_2d(B + 8192, &a.tmB, bar, g.n0 + half * rank + 64, r);
                     } else {
                         // the loads of both CTAs complete on the first one's barrier
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                        const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                        const uint32_t bar = full0 + s * 8;
                         if constexpr (OP == kOpGemm) {
                             tma_pair_3d(A, &a.tmA, bar, kb * kBK, m0, g.e);
                         } else {
                             tma_pair_3d(A, &a.tmA, bar, m0, kb * kBK, g.e);
                             tma_pair_3d(A + 8192, &a.tmA, bar, m0 + 64, kb * kBK, g.e);
                         }
-                        for (int j = 0; j < nb; ++j)
-                            tma_pair_2d(B + j * kBoxRows * kKBytes, &a.tmB, bar, kb * kBK,
-                                        g.row0 + half * rank + kBoxRows * j);
+                        if (big) {
+                            tma_pair_2d(B, &a.tmB128, bar, kb * kBK, r0);
+                        } else {
+                            for (int j = 0; j < nb; ++j)
+                                tma_pair_2d(B + j * kBoxRows * kKBytes, &a.tmB, bar, kb * kBK, r0 + kBoxRows * j);
+                        }
                     }
                 }
+                if (used < kStages) ++used;
+                if (++s == kStages) { s = 0; phase ^= 1; }
             }
-            // every issued stage released by the MMAs: no commit arrives in
-            // this CTA's shared memory after it exits
-            const uint32_t first = it > static_cast<uint32_t>(kStages) ? it - kStages : 0u;
-            for (uint32_t q = first; q < it && ok; ++q)
-                if (!mbar_wait_bounded(&empty[q % kStages], (q / kStages) & 1)) {
-                    fail();
-                    break;
-                }
         }
+        // every issued stage released by the MMAs: no commit arrives in
+        // this CTA's shared memory after it exits
+        for (; used > 0; --used) {
+            if (s == 0) { s = kStages; phase ^= 1; }
+            --s;
+            stop |= !wait(empty_u + s * 8, phase ^ 1);
+        }
+        if (stop) __nanosleep(1000000);          // what was still in flight lands
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA
-        if (lane == 0 && rank == 0) {
-            uint32_t it = 0;
-            int local = 0;
-            bool ok = true;
-            for (; ok && !*abort_flag && walk.next(g); ++local) {
+        // the whole warp runs the loop, so that the descriptors are computed
+        // for the warp and not for a lane; one lane issues
+        if (rank == 0) {
+            // descriptors of the first stage; a stage or k-slice further is an
+            // addition to the address field (no carry: 227 KB / 16 < 2^14)
+            const uint64_t a0 = OP == kOpGemm ? umma_desc_sw128(ring_base) : umma_desc_mn_sw128(ring_base);
+            const uint64_t b0 = OP == kOpWgrad ? umma_desc_mn_sw128(ring_base + kStageHalf)
+                                               : umma_desc_sw128(ring_base + kStageHalf);
+            constexpr uint32_t kStepA = (OP == kOpGemm ? 32 : 2048) / 16, kStepB = (OP == kOpWgrad ? 2048 : 32) / 16;
+            int s = 0, local = 0;
+            uint32_t phase = 0;
+            uint32_t pad_phase = 0;                  // a bit for each stage: uses of its padded[]
+            for (; walk.next(g); ++local) {
                 const int b = local & 1;
-                if (local >= 2 && !mbar_wait_cluster(&tempty[b], ((local >> 1) - 1) & 1)) {
-                    fail();
-                    break;
-                }
+                wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + b * kTile;
                 const uint32_t idesc = a.idesc | (static_cast<uint32_t>(g.cols >> 3) << 17);
-                for (int kb = 0; kb < g.nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (*abort_flag || !mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
-                        fail();
-                        ok = false;
-                        break;
+                // wgrad: 16-row slices of the last step, and whether it is padded
+                const int last = OP == kOpWgrad ? (((g.valid - 1) & 63) >> 4) + 1 : 4;
+                const int n_full = OP == kOpWgrad && (g.valid & 63) ? g.nk - 1 : g.nk;
+                for (int kb = 0; kb < n_full; ++kb) {
+                    wait(full_u + s * 8, phase);
+                    tc_fence_after();
+                    const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
+                    const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk ? 1u : kb != 0);
+                        umma_commit_pair(&empty[s]);
+                    }
+                    if (++s == kStages) { s = 0; phase ^= 1; }
+                }
+                if (n_full < g.nk) {
+                    wait(full_u + s * 8, phase);
+                    if (g.valid & 15) {
+                        wait(padded_u + s * 8, (pad_phase >> s) & 1);
+                        pad_phase ^= 1u << s;
                     }
                     tc_fence_after();
-                    const uint32_t A = smem_u32(ring + s * kStage);
-                    const uint32_t B = A + kStageHalf;
-                    if constexpr (OP == kOpWgrad) {
-                        const int steps = min(4, (g.valid - kb * 64 + 15) / 16);
-                        for (int kk = 0; kk < steps; ++kk)
-                            umma_pair<false>(d_tmem, umma_desc_mn_sw128(A + kk * 2048),
-                                             umma_desc_mn_sw128(B + kk * 2048), idesc, (kb | kk) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t ad = OP == kOpGemm ? umma_desc_sw128(A + kk * 32)
-                                                              : umma_desc_mn_sw128(A + kk * 2048);
-                            umma_pair<I8>(d_tmem, ad, umma_desc_sw128(B + kk * 32), idesc,
-                                          (kb | kk) ? 1u : 0u);
-                        }
+                    const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
+                    const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
+                    if (elect_one()) {
+                        for (int kk = 0; kk < last; ++kk)
+                            umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk || n_full ? 1u : 0u);
+                        umma_commit_pair(&empty[s]);
                     }
-                    umma_commit_pair(&empty[s]);
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
-                if (ok) umma_commit_pair(&tfull[b]);
+                if (elect_one()) umma_commit_pair(&tfull[b]);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 2 + kEpiWarps) {
         // ----------------------------------------------------- epilogue
         const int q = warp & 3;                        // TMEM lane quarter of this warp
-        int local = 0, n_box = 0;
+        const int part = (warp - 2) >> 2;              // of the quarter's two warps
+        const uint32_t own = smem_u32(epi) + (warp - 2) * 128;       // 8 bits: 32 tokens' scales
+        int local = 0;
         for (; walk.next(g); ++local) {
             // every decision before the warp-collective tcgen05.ld is warp-uniform
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             const int b = local & 1;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tfull[b], (local >> 1) & 1));
-            if (!ok) {
-                if (lane == 0) fail();
-                break;
-            }
+            if (__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1))) continue;
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile;
             const int f0 = g.m0 + kHalf * rank + q * 32;      // this warp's first feature
-            if constexpr (OP == kOpWgrad) {
-                // 32 rows x 128 bytes at a time through shared memory: each
-                // thread writes its row's 16-byte chunks XOR-swizzled (as the
-                // store's map reads them), then one TMA store per box
-                const int per = a.out_dtype == MOE_DTYPE_F32 ? 32 : 64;
-                const uint32_t stg = smem_u32(epi) + (warp - 2) * 2 * kEpiBox;
-                const uint32_t row = stg + lane * 128;
-                for (int c = 0; c < g.cols && f0 < a.M && (g.nk || !a.accumulate); c += per, ++n_box) {
-                    uint32_t v[32], p[32];
-                    if (g.nk) tmem_ld32(taddr + c, v);
-                    tmem_ld_wait();
-                    if (per == 64) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
-                            p[i] = a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-                        }
-                        if (g.nk && c + 32 < g.cols) tmem_ld32(taddr + c + 32, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
-                            p[16 + i] = a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) p[i] = v[i];
-                    }
-                    if (g.nk == 0) {               // an expert without rows
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) p[i] = 0u;
-                    }
-                    // the box of two rounds ago has left shared memory
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
-                    const uint32_t buf = (n_box & 1) * kEpiBox;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(row + buf + ((j ^ (lane & 7)) * 16)), "r"(p[4 * j]),
-                                       "r"(p[4 * j + 1]), "r"(p[4 * j + 2]), "r"(p[4 * j + 3]) : "memory");
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (g.n0 + c < a.N) tma_store_3d(&a.tmD, stg + buf, g.n0 + c, f0, g.e, a.accumulate != 0);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                }
-            } else {
-                const int f = f0 + lane;
-                const float ws = I8 && f < a.M ? a.w_scale[static_cast<int64_t>(g.e) * a.M + f] : 1.f;
+            const int f = f0 + lane;
+            const float ws = I8 && f < a.M ? a.w_scale[static_cast<int64_t>(g.e) * a.M + f] : 1.f;
+            // columns: tokens, or (wgrad) rows of the expert's dW
+            const int valid = OP == kOpWgrad ? min(kTile, a.N - g.n0) : g.valid;
+            const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
 #pragma unroll 1
-                for (int c = 0; c < g.valid; c += 32) {
-                    uint32_t v[32];
+            for (int c = part * 32; c < valid && f0 < a.M; c += 64) {
+                uint32_t v[32];
+                if (OP == kOpWgrad && g.nk == 0) {            // an expert without rows
+                    if (a.accumulate) break;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                } else {
                     tmem_ld32(taddr + c, v);
+                }
+                const int64_t r0 = col0 + c;
+                const int n = valid - c;                      // columns to store, if below 32
+                if constexpr (I8) {
+                    // the tokens' scales, four to a load from shared memory
+                    const float as = lane < n ? a.a_scale[r0 + lane] : 0.f;
+                    __syncwarp();
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + lane * 4), "f"(as) : "memory");
+                    __syncwarp();
                     tmem_ld_wait();
-                    const int64_t r0 = static_cast<int64_t>(g.row0) + c;
-                    if constexpr (I8) {
-                        const float as = c + lane < g.valid ? a.a_scale[r0 + lane] : 0.f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = __float_as_uint(static_cast<float>(static_cast<int>(v[i])) *
-                                                   __shfl_sync(0xffffffffu, as, i) * ws);
+                    for (int i = 0; i < 32; i += 4) {
+                        float k[4];
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3]) : "r"(own + i * 4));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[i + j] = __float_as_uint(static_cast<float>(static_cast<int>(v[i + j])) * k[j] * ws);
                     }
-                    if (a.out_dtype == MOE_DTYPE_F32) {
-                        float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
+                } else {
+                    tmem_ld_wait();
+                }
+                if (a.out_dtype == MOE_DTYPE_F32) {
+                    float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
+                    if (OP == kOpWgrad && a.accumulate) {
+                        // each element has one owner: one addition, in no one's order
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < g.valid && f < a.M) o[i * a.out_stride] = __uint_as_float(v[i]);
+                        for (int i = 0; i < 32; ++i, o += a.out_stride)
+                            if (i < n && f < a.M) red_add_f32(o, __uint_as_float(v[i]));
                     } else {
-                        // neighbouring lanes (features) trade columns, so that
-                        // each stores two features of one token: 4 bytes
-                        const int odd = lane & 1;
-                        uint16_t* o = static_cast<uint16_t*>(a.out) + (r0 + odd) * a.out_stride + (f & ~1);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                            const float lo = __uint_as_float(odd ? got : v[i]);
-                            const float hi = __uint_as_float(odd ? v[i + 1] : got);
-                            if (c + i + odd < g.valid && f < a.M)
-                                *reinterpret_cast<uint32_t*>(o + i * a.out_stride) =
-                                    a.out_dtype == MOE_DTYPE_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
-                        }
+                        for (int i = 0; i < 32; ++i, o += a.out_stride)
+                            if (i < n && f < a.M) *o = __uint_as_float(v[i]);
                     }
+                } else if (f < a.M) {                         // M is even: both lanes of a pair or neither
+                    store_pairs(static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1), a.out_stride, v, n,
+                                a.out_dtype == MOE_DTYPE_F16, f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_u + b * 8, 0));
         }
-        if (OP == kOpWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
-        // wgrad: hands each stage to the MMA warp once this CTA's loads have
-        // landed, with the rows past the segment's end zeroed
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && walk.next(g)) {
-            for (int kb = 0; kb < g.nk; ++kb, ++it) {
-                const int s = it % kStages;
-                ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(&landed[s], (it / kStages) & 1));
-                if (!ok) {
-                    if (lane == 0) fail();
-                    break;
-                }
-                const int left = g.valid - kb * 64;
-                const int pad = left < 64 ? (-left & 15) : 0;      // rows left .. left + pad - 1
-                if (pad) {
-                    const uint32_t base = smem_u32(ring + s * kStage) + left * 128;
-                    for (int j = lane; j < pad * 8 * 4; j += 32) {  // four boxes of 64 columns
-                        const uint32_t at = base + (j / (pad * 8)) * 8192 + (j % (pad * 8)) * 16;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+        // wgrad: zeros the rows past a segment's end in its last step, up to
+        // the next multiple of the MMA's 16, once this CTA's loads have landed
+        uint32_t it = 0, phase = 0;
+        while (walk.next(g)) {
+            it += g.nk;
+            const int pad = -g.valid & 15;
+            if (pad == 0 || g.nk == 0) continue;
+            const int s = (it - 1) % kStages;
+            if (__any_sync(0xffffffffu, !wait(landed_u + s * 8, (phase >> s) & 1))) break;
+            phase ^= 1u << s;
+            const uint32_t base = ring_base + s * kStage + (g.valid & 63) * 128;
+            for (int j = lane; j < pad * 8 * 4; j += 32) {          // four boxes of 64 columns
+                const uint32_t at = base + (j / (pad * 8)) * 8192 + (j % (pad * 8)) * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
             }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(padded_u + s * 8, 0));
         }
     }
     tc_fence_before();
@@ -529,8 +559,8 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 
 template <int OP>
 size_t tc_smem_bytes(int E) {
-    return 1024 + kStages * kStage + (3 * kStages + 4) * 8 + 8 +
-           (OP == kOpWgrad ? kEpiBytes : 2 * (static_cast<size_t>(E) + 1) * 4);
+    return 1024 + kStages * kStage + (4 * kStages + 4) * 8 + 8 +
+           kEpiBytes + (OP == kOpWgrad ? 0 : 2 * (static_cast<size_t>(E) + 1) * 4);
 }
 
 // ================================================================= host ===
@@ -655,6 +685,12 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
     if (c.dtype != MOE_DTYPE_F16) a.idesc |= (1u << 7) | (1u << 10);
     bool ok = true;
     int64_t tiles = 0;
+    if (op != kOpWgrad) {
+        // weight tiles that take 32 MB, a quarter of L2
+        const int64_t k_bytes = static_cast<int64_t>(op == kOpGemm ? c.d_in : c.d_out) * elem;
+        const int64_t mb = (32 << 20) / (kTile * k_bytes);
+        a.m_block = static_cast<int>(mb < 1 ? 1 : mb > 64 ? 64 : mb);
+    }
     const int64_t chunks = ceil_div(c.rows, kTile) + (c.rows < c.E ? c.rows : c.E);   // at most
     if (op == kOpGemm) {
         a.M = c.d_out;
@@ -662,6 +698,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         a.out_stride = c.y_stride;
         ok &= stack_map(&a.tmA, elem, c.w, c.d_in, c.d_out, c.E, bk, kHalf);
         ok &= rows_map(&a.tmB, elem, c.a, c.d_in, c.rows, c.x_stride, bk, kBoxRows);
+        ok &= rows_map(&a.tmB128, elem, c.a, c.d_in, c.rows, c.x_stride, bk, 128);
         tiles = chunks * ceil_div(a.M, kTile);
     } else if (op == kOpDgrad) {
         a.M = c.d_in;
@@ -670,15 +707,15 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         a.idesc |= 1u << 15;                               // A MN-major
         ok &= stack_map(&a.tmA, elem, c.w, c.d_in, c.d_out, c.E, 64, 64);
         ok &= rows_map(&a.tmB, elem, c.a, c.d_out, c.rows, c.y_stride, bk, kBoxRows);
+        ok &= rows_map(&a.tmB128, elem, c.a, c.d_out, c.rows, c.y_stride, bk, 128);
         tiles = chunks * ceil_div(a.M, kTile);
     } else {
-        a.M = c.d_out;
-        a.N = c.d_in;
+        a.M = c.d_in;
+        a.N = c.d_out;
+        a.out_stride = c.d_in;
         a.idesc |= (1u << 15) | (1u << 16);                // A and B MN-major
-        ok &= rows_map(&a.tmA, elem, c.a, c.d_out, c.rows, c.y_stride, 64, 64);
-        ok &= rows_map(&a.tmB, elem, c.w, c.d_in, c.rows, c.x_stride, 64, 64);
-        const int oe = c.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
-        ok &= stack_map(&a.tmD, oe, c.out, c.d_in, c.d_out, c.E, 128 / oe, 32);
+        ok &= rows_map(&a.tmA, elem, c.w, c.d_in, c.rows, c.x_stride, 64, 64);
+        ok &= rows_map(&a.tmB, elem, c.a, c.d_out, c.rows, c.y_stride, 64, 64);
         tiles = static_cast<int64_t>(c.E) * ceil_div(a.M, kTile) * ceil_div(a.N, kTile);
     }
     if (!ok) return MOE_ERR_INVALID_ARG;
