@@ -38,6 +38,8 @@ static __device__ uint32_t g_grouped_err;
 
 namespace {
 
+#include "grouped_small.cuh"
+
 constexpr int kMaxDevices = 64;
 constexpr int kTile = 256;                        // tile rows (M), and the most columns (N)
 constexpr int kHalf = 128;                        // rows of the tile one CTA holds
@@ -659,6 +661,18 @@ moe_status_t launch_tc(const TcArgs& a, int64_t tiles, cudaStream_t stream) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Whether a product goes to grouped_small_kernel: its 256-row weight tiles keep
+// at most half of the CTA pairs busy, and its experts average at most 16 rows
+// (a second pass over weights that L1 and L2 hold).  Measured, small / tensor
+// cores: 8 experts of 2048 x 1024, a row each (32 tiles) 9.9 / 13.8 us; one of
+// 4096 x 4096 (16 tiles) with 1 row 7.9 / 19.0 us, with 32 rows 24.9 / 19.1 us; 16
+// experts of 2048 x 1024 (64 tiles) 18.8 / 16.6 us, 8 of 512 x 2048 (64 tiles) 10.1
+// / 8.2 us, 2 of 4096 x 28672 (224 tiles) 99 / 91 us.
+bool few_rows(const GroupedCall& c) {
+    const int64_t slots = c.rows < c.E ? c.rows : c.E;      // experts with rows, at most
+    return slots * ceil_div(c.d_out, kTile) <= 37 && c.rows <= 16 * slots;
+}
+
 }  // namespace
 
 moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t stream) {
@@ -669,6 +683,28 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         if (op != kOpWgrad || c.accumulate) return MOE_OK;
         const size_t n = static_cast<size_t>(c.E) * c.d_out * c.d_in * (c.out_dtype == MOE_DTYPE_F32 ? 4 : 2);
         return cudaMemsetAsync(c.out, 0, n, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    if (op == kOpGemm && few_rows(c)) {
+        SmallArgs m{};
+        m.offsets = c.offsets;
+        m.x = static_cast<const uint8_t*>(c.a);
+        m.w = static_cast<const uint8_t*>(c.w);
+        m.out = c.out;
+        m.a_scale = c.a_scale;
+        m.w_scale = c.w_scale;
+        m.x_bytes = c.x_stride * elem;
+        m.out_stride = c.y_stride;
+        m.rows = c.rows;
+        m.E = c.E;
+        m.M = c.d_out;
+        m.k_bytes = c.d_in * elem;
+        m.f16 = c.dtype == MOE_DTYPE_F16;
+        m.out_dtype = c.out_dtype;
+        const int64_t units = ceil_div(c.d_out, kSmallRows) * (c.rows < c.E ? c.rows : c.E);    // at most
+        const unsigned grid = static_cast<unsigned>(units < 2 * 148 ? units : 2 * 148);
+        if (i8) grouped_small_kernel<true><<<grid, kSmallThreads, 0, stream>>>(m);
+        else grouped_small_kernel<false><<<grid, kSmallThreads, 0, stream>>>(m);
+        return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     TcArgs a;
     memset(&a, 0, sizeof(a));

@@ -1,8 +1,9 @@
 // rows.cu -- the row operators around the experts' products: SwiGLU, its
 // gradient, and the rounding of rows to 8-bit codes with a scale for each row.
 //
-// All are bound by the bytes they read and write.  Every thread moves 16-byte
-// vectors (8 elements), computes in fp32 and rounds each result once.
+// All are bound by the bytes they read and write, if the arithmetic stays
+// small beside them: every thread moves 16-byte vectors (8 elements), computes
+// in fp32 and rounds each result once.
 #include "grouped.cuh"
 
 namespace moe {
@@ -33,24 +34,64 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
         w[i] = F16 ? pack_f16x2(f[2 * i], f[2 * i + 1]) : pack_bf16x2(f[2 * i], f[2 * i + 1]);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// sigmoid: e^-g is +inf for g < -88.7, and 1 / (1 + inf) = 0, its limit
-__device__ __forceinline__ float sigmoid_f(float g) { return 1.f / (1.f + expf(-g)); }
+// sigmoid(g) = 1 / (1 + 2^t), t = -g log2(e).  t is formed in two parts, since
+// the rounding of t alone would cost |g| half steps of the result: 2^t =
+// 2^hi (1 + lo ln 2).  Errors in units of 2^-24: 2^hi 4 (ex2.approx), 1 + lo
+// ln 2 and the product 1 each, 1 + 2^t 1, the reciprocal 2: at most 9.  For g <
+// -88.7 the power is infinite and the result 0, as with any fp32 exponential;
+// lo is dropped where t is so large (it would be NaN at an infinity).
+__device__ __forceinline__ float sigmoid_f(float g) {
+    constexpr float kL = -1.44269504f, kLlo = -1.92596299e-8f, kLn2 = 0.693147181f;
+    const float hi = g * kL;
+    float lo = fmaf(g, kLlo, fmaf(g, kL, -hi));
+    lo = fabsf(hi) < 256.f ? lo : 0.f;
+    float p, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(hi));
+    p *= fmaf(lo, kLn2, 1.f);
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
+    return r;
+}
+
+// Vector i of `n` as a row and a first column, for fewer than 2^31 vectors:
+// i / vec by a multiplication (d = vec: mul = floor(2^32 (2^s - d) / d) + 1,
+// s = ceil(log2 d); the quotient is then (umulhi(mul, i) + i) >> s).
+struct FastDiv {
+    uint32_t d, mul, s;
+    explicit FastDiv(uint32_t v) : d(v), s(0) {
+        while ((uint64_t(1) << s) < d) ++s;
+        mul = static_cast<uint32_t>((((uint64_t(1) << s) - d) << 32) / d + 1);
+    }
+};
+template <bool BIG>
+__device__ __forceinline__ void place(int64_t i, const FastDiv& f, int64_t& r, int& col) {
+    if (BIG) {
+        r = i / f.d;
+        col = static_cast<int>(i - r * f.d) * 8;
+    } else {
+        const uint32_t k = static_cast<uint32_t>(i);
+        const uint32_t q = (__umulhi(f.mul, k) + k) >> f.s;
+        r = q;
+        col = static_cast<int>(k - q * f.d) * 8;
+    }
+}
 
 // h = g sig(g) u.  g = -inf gives -inf * 0 = NaN, as the formula does.
-template <bool F16>
-__global__ void __launch_bounds__(kRowThreads) swiglu_kernel(const RowsCall c) {
-    const int vec = c.cols / 8;
-    const int64_t n = c.rows * vec;
+template <bool F16, bool BIG>
+__global__ void __launch_bounds__(kRowThreads) swiglu_kernel(const RowsCall c, const FastDiv f) {
+    const int64_t n = c.rows * f.d;
     const uint16_t* gate = static_cast<const uint16_t*>(c.a);
     const uint16_t* up = static_cast<const uint16_t*>(c.b);
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kRowThreads) + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
-        const int64_t r = i / vec;
-        const int col = static_cast<int>(i - r * vec) * 8;
+        int64_t r;
+        int col;
+        place<BIG>(i, f, r, col);
+        const uint4 vg = load16(gate + r * c.in_stride + col), vu = load16(up + r * c.in_stride + col);
         float g[8], u[8];
-        unpack8<F16>(*reinterpret_cast<const uint4*>(gate + r * c.in_stride + col), g);
-        unpack8<F16>(*reinterpret_cast<const uint4*>(up + r * c.in_stride + col), u);
+        unpack8<F16>(vg, g);
+        unpack8<F16>(vu, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid_f(g[j]) * u[j];
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + r * c.out_stride + col) = pack8<F16>(g);
@@ -58,21 +99,23 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(const RowsCall c) {
 }
 
 // dgate = dh u sig(g) (1 + g (1 - sig(g))),  dup = dh g sig(g)
-template <bool F16>
-__global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall c) {
-    const int vec = c.cols / 8;
-    const int64_t n = c.rows * vec;
+template <bool F16, bool BIG>
+__global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall c, const FastDiv f) {
+    const int64_t n = c.rows * f.d;
     const uint16_t* gate = static_cast<const uint16_t*>(c.a);
     const uint16_t* up = static_cast<const uint16_t*>(c.b);
     const uint16_t* dh = static_cast<const uint16_t*>(c.dh);
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kRowThreads) + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
-        const int64_t r = i / vec;
-        const int col = static_cast<int>(i - r * vec) * 8;
+        int64_t r;
+        int col;
+        place<BIG>(i, f, r, col);
+        const uint4 vg = load16(gate + r * c.in_stride + col), vu = load16(up + r * c.in_stride + col);
+        const uint4 vd = load16(dh + r * c.dh_stride + col);
         float g[8], u[8], d[8];
-        unpack8<F16>(*reinterpret_cast<const uint4*>(gate + r * c.in_stride + col), g);
-        unpack8<F16>(*reinterpret_cast<const uint4*>(up + r * c.in_stride + col), u);
-        unpack8<F16>(*reinterpret_cast<const uint4*>(dh + r * c.dh_stride + col), d);
+        unpack8<F16>(vg, g);
+        unpack8<F16>(vu, u);
+        unpack8<F16>(vd, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float s = sigmoid_f(g[j]);
@@ -86,6 +129,30 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall
     }
 }
 
+// Codes of 8 values v: q = rint(v / s), the quotient rounded to nearest first.
+// v * (1 / s) is within 127 * 3 * 2^-24 < 2.3e-5 of that quotient (the sum and
+// the difference below are rounded once each), so it rounds
+// to the same integer unless it lies within 3e-5 of a half; only then is the
+// division done.  Adding 1.5 * 2^23 rounds to the nearest
+// integer, ties to even, and leaves it in the low byte.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float inv) {
+    constexpr float kMagic = 12582912.f;
+    uint32_t b[8];
+    float off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = fmaf(v[i], inv, kMagic);
+        off = fmaxf(off, fabsf(fmaf(v[i], inv, kMagic - t)));
+        b[i] = __float_as_uint(t);
+    }
+    if (off > 0.49997f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], s)))));
+    }
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
 // Codes of a row v (x itself, or SwiGLU of gate and up, in fp32): with
 // a = max |v|, s = a / 127 and q = rint(v / s), both divisions rounded to
 // nearest (the codes are then those of any fp32 evaluation of the formula).
@@ -93,7 +160,8 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall
 // so that the product shows it.  |v| is compared by its bits: a NaN is larger
 // than an infinity, and an infinity than every number.
 // TPR threads share a row, each keeping up to VPT vectors of it in registers
-// between the two passes; what a longer row has beyond that is read again.
+// between the two passes (as they were loaded; SwiGLU's as computed); what a
+// longer row has beyond that is read again.
 template <bool F16, bool GLU, int TPR, int VPT>
 __global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) {
     constexpr int kRows = kRowThreads / TPR;          // rows of a block
@@ -105,29 +173,56 @@ __global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) 
     const uint16_t* pa = static_cast<const uint16_t*>(c.a) + (live ? r : 0) * c.in_stride;
     const uint16_t* pb = GLU ? static_cast<const uint16_t*>(c.b) + (live ? r : 0) * c.in_stride : nullptr;
 
-    auto value = [&](int j, float (&f)[8]) {
-        unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(pa + j * 8)), f);
-        if constexpr (GLU) {
-            float u[8];
-            unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(pb + j * 8)), u);
+    auto glu = [&](const uint4& va, const uint4& vb, float (&f)[8]) {
+        float u[8];
+        unpack8<F16>(va, f);
+        unpack8<F16>(vb, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid_f(f[i]) * u[i];
-        }
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid_f(f[i]) * u[i];
     };
-    uint32_t m = 0;
+    // |v| of 16-bit values order by their bits, two to an instruction
+    uint32_t m = 0, m2 = 0;
+    auto widen16 = [&](const uint4& v) {
+        m2 = __vmaxu2(m2, v.x & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v.y & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v.z & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v.w & 0x7FFF7FFFu);
+    };
     auto widen = [&](const float (&f)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
     };
-    float keep[VPT][8];
+    uint4 raw[VPT], raw_b[GLU ? VPT : 1];
+    float val[GLU ? VPT : 1][8];
     if (live) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
-            if (t + v * TPR < vec) { value(t + v * TPR, keep[v]); widen(keep[v]); }
+            if (t + v * TPR < vec) {
+                raw[v] = load16(pa + (t + v * TPR) * 8);
+                if constexpr (GLU) raw_b[v] = load16(pb + (t + v * TPR) * 8);
+            }
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (t + v * TPR < vec) {
+                if constexpr (GLU) {
+                    glu(raw[v], raw_b[v], val[v]);
+                    widen(val[v]);
+                } else {
+                    widen16(raw[v]);
+                }
+            }
         for (int j = t + VPT * TPR; j < vec; j += TPR) {
-            float f[8];
-            value(j, f);
-            widen(f);
+            if constexpr (GLU) {
+                float f[8];
+                glu(load16(pa + j * 8), load16(pb + j * 8), f);
+                widen(f);
+            } else {
+                widen16(load16(pa + j * 8));
+            }
+        }
+        if constexpr (!GLU) {
+            const unsigned short top = static_cast<unsigned short>(max(m2 & 0xFFFFu, m2 >> 16));
+            m = F16 ? __float_as_uint(__half2float(__ushort_as_half(top))) : static_cast<uint32_t>(top) << 16;
         }
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -143,56 +238,85 @@ __global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) 
     const float s = finite ? __fdiv_rn(__uint_as_float(m), 127.f) : __uint_as_float(0x7FC00000u);
     if (t == 0) c.scale[r] = s;
     int8_t* q = static_cast<int8_t*>(c.out) + r * c.out_stride;
+    // a scale below 2^-100 (its reciprocal and its own rounding are no longer
+    // good for the bound above) takes the division for every value
+    const bool fast = s > 7.8886091e-31f;
+    const float inv = fast ? __fdiv_rn(1.f, s) : 0.f;
     auto store = [&](int j, const float (&f)[8]) {
-        uint32_t w[2] = {0u, 0u};
-        if (finite && s > 0.f) {
+        uint2 w = make_uint2(0u, 0u);
+        if (fast) {
+            w = codes8(f, s, inv);
+        } else if (finite && s > 0.f) {
+            uint32_t b[2] = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int code = max(-127, min(127, __float2int_rn(__fdiv_rn(f[i], s))));
-                w[i >> 2] |= (static_cast<uint32_t>(code) & 0xFFu) << (8 * (i & 3));
+                b[i >> 2] |= (static_cast<uint32_t>(code) & 0xFFu) << (8 * (i & 3));
             }
+            w = make_uint2(b[0], b[1]);
         }
-        *reinterpret_cast<uint2*>(q + j * 8) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(q + j * 8) = w;
     };
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-        if (t + v * TPR < vec) store(t + v * TPR, keep[v]);
+        if (t + v * TPR < vec) {
+            if constexpr (GLU) {
+                store(t + v * TPR, val[v]);
+            } else {
+                float f[8];
+                unpack8<F16>(raw[v], f);
+                store(t + v * TPR, f);
+            }
+        }
     for (int j = t + VPT * TPR; j < vec; j += TPR) {
         float f[8];
-        value(j, f);
+        if constexpr (GLU) glu(load16(pa + j * 8), load16(pb + j * 8), f);
+        else unpack8<F16>(load16(pa + j * 8), f);
         store(j, f);
     }
 }
 
+template <bool F16, bool GLU, int TPR, int VPT>
+void i8_rows_launch(const RowsCall& c, cudaStream_t stream) {
+    const int64_t blocks = (c.rows + kRowThreads / TPR - 1) / (kRowThreads / TPR);
+    i8_rows_kernel<F16, GLU, TPR, VPT><<<static_cast<unsigned>(blocks), kRowThreads, 0, stream>>>(c);
+}
+
 template <bool F16, bool GLU>
 cudaError_t i8_rows(const RowsCall& c, cudaStream_t stream) {
-    // a warp for a row of up to 1024 elements; a block for longer ones
-    if (c.cols <= 1024) {
-        const int64_t blocks = (c.rows + 7) / 8;
-        i8_rows_kernel<F16, GLU, 32, 4><<<static_cast<unsigned>(blocks), kRowThreads, 0, stream>>>(c);
-    } else {
-        i8_rows_kernel<F16, GLU, 256, 4><<<static_cast<unsigned>(c.rows), kRowThreads, 0, stream>>>(c);
+    // as few threads to a row as hold it with four vectors each, but no fewer
+    // than give the device a block for each SM
+    int tpr = 32;
+    while (tpr < 256 && (c.cols > tpr * 32 || c.rows * tpr < 148 * kRowThreads)) tpr *= 2;
+    switch (tpr) {
+        case 32: i8_rows_launch<F16, GLU, 32, 4>(c, stream); break;
+        case 64: i8_rows_launch<F16, GLU, 64, 4>(c, stream); break;
+        case 128: i8_rows_launch<F16, GLU, 128, 4>(c, stream); break;
+        default: i8_rows_launch<F16, GLU, 256, 4>(c, stream); break;
     }
     return cudaGetLastError();
 }
 
-unsigned flat_blocks(const RowsCall& c) {
-    const int64_t n = (c.rows * (c.cols / 8) + kRowThreads - 1) / kRowThreads;
-    return static_cast<unsigned>(n < 148 * 64 ? n : 148 * 64);
+template <typename K>
+cudaError_t flat(K small, K big, const RowsCall& c, cudaStream_t stream) {
+    const int64_t n = c.rows * (c.cols / 8);
+    const int64_t blocks = (n + kRowThreads - 1) / kRowThreads;
+    const unsigned grid = static_cast<unsigned>(blocks < 148 * 64 ? blocks : 148 * 64);
+    (n < (int64_t(1) << 31) ? small : big)<<<grid, kRowThreads, 0, stream>>>(c, FastDiv(c.cols / 8));
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu(const RowsCall& c, cudaStream_t stream) {
-    if (c.dtype == MOE_DTYPE_F16) swiglu_kernel<true><<<flat_blocks(c), kRowThreads, 0, stream>>>(c);
-    else swiglu_kernel<false><<<flat_blocks(c), kRowThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+    return c.dtype == MOE_DTYPE_F16 ? flat(swiglu_kernel<true, false>, swiglu_kernel<true, true>, c, stream)
+                                    : flat(swiglu_kernel<false, false>, swiglu_kernel<false, true>, c, stream);
 }
 
 cudaError_t launch_swiglu_grad(const RowsCall& c, cudaStream_t stream) {
-    if (c.dtype == MOE_DTYPE_F16) swiglu_grad_kernel<true><<<flat_blocks(c), kRowThreads, 0, stream>>>(c);
-    else swiglu_grad_kernel<false><<<flat_blocks(c), kRowThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+    return c.dtype == MOE_DTYPE_F16
+               ? flat(swiglu_grad_kernel<true, false>, swiglu_grad_kernel<true, true>, c, stream)
+               : flat(swiglu_grad_kernel<false, false>, swiglu_grad_kernel<false, true>, c, stream);
 }
 
 cudaError_t launch_i8_rows(const RowsCall& c, cudaStream_t stream) {
