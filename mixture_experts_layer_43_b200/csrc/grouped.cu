@@ -129,6 +129,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+// Arrive on a barrier of either CTA without waiting for this thread's global
+// stores (which a release at cluster scope would): what it hands over is tensor
+// memory, ordered by the tcgen05 fences.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // The rest of a wait whose first poll failed: at most kWaitLimitNs, and over at
 // once when another wait of this CTA has run out.
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -222,38 +228,58 @@ struct TileWalk {
     }
 };
 
-// Offsets into shared memory, checked; and the running count of row chunks.
-// Returns false (for every thread of the block) if the table is not sound.
 template <int OP>
-__device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base) {
+constexpr int tc_threads() { return (2 + kEpiWarps + (OP == kOpWgrad ? 1 : 0)) * 32; }
+
+// Offsets into shared memory, checked; and the running count of row chunks: each
+// thread takes kPer experts in a row, then a scan over the warps.  Returns false
+// (for every thread of the block) if the table is not sound.
+template <int OP>
+__device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base, int* s_warp) {
+    constexpr int kPer = 4;
+    static_assert(kPer * tc_threads<OP>() >= kMaxExperts, "every expert has a thread");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e0 = static_cast<int>(threadIdx.x) * kPer;
     bool bad = false;
-    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
-        const int v = a.offsets[e];
-        const int next = e < a.E ? a.offsets[e + 1] : v;
-        bad |= v < 0 || v > a.rows || next < v;
-        if (OP != kOpWgrad) s_off[e] = v;
-    }
-    bad = __syncthreads_or(bad);
-    if (!bad && OP != kOpWgrad && threadIdx.x < 32) {
-        int sum = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + static_cast<int>(threadIdx.x);
-            int c = e < a.E ? (s_off[e + 1] - s_off[e] + kTile - 1) / kTile : 0;
+    int v[kPer + 1], count[kPer], sum = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, c, d);
-                if (static_cast<int>(threadIdx.x) >= d) c += o;
-            }
-            if (e < a.E) s_base[e + 1] = sum + c;
-            sum += __shfl_sync(0xffffffffu, c, 31);
+    for (int i = 0; i <= kPer; ++i) v[i] = e0 + i <= a.E ? a.offsets[e0 + i] : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        count[i] = 0;
+        if (e0 + i < a.E) {
+            bad |= v[i] < 0 || v[i] > a.rows || v[i + 1] > a.rows || v[i + 1] < v[i];
+            count[i] = (v[i + 1] - v[i] + kTile - 1) / kTile;
         }
-        if (threadIdx.x == 0) s_base[0] = 0;
+        sum += count[i];
+    }
+    if (OP == kOpWgrad) {
+        bad = __syncthreads_or(bad);
+        return !bad;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (e0 + i <= a.E) s_off[e0 + i] = v[i];
+    if (a.E == kMaxExperts && e0 + kPer == a.E) s_off[a.E] = v[kPer];
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    bad = __syncthreads_or(bad);
+    int before = upto - sum;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (e0 + i < a.E) s_base[e0 + i] = before;
+        before += count[i];
+        if (e0 + i == a.E - 1) s_base[a.E] = before;
     }
     return !bad;
 }
 
-template <int OP>
-constexpr int tc_threads() { return (2 + kEpiWarps + (OP == kOpWgrad ? 1 : 0)) * 32; }
 
 // 32 columns (tokens) of this lane's feature as 16-bit values, `n` of them
 // stored: even and odd lanes trade half of their packed pairs of tokens, so
@@ -281,6 +307,46 @@ __device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const
     }
 }
 
+// 32 accumulator columns (tokens r0 .. of gemm and dgrad, rows of dW in wgrad),
+// n of them if below 32, of this lane's feature f; f0 is lane 0's.
+template <int OP, bool I8>
+__device__ __forceinline__ void store_columns(const TcArgs& a, uint32_t (&v)[32], int64_t r0, int n, int f, int f0,
+                                              float ws, uint32_t own) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (I8) {
+        // the tokens' scales, four to a load from shared memory
+        const float as = lane < n ? a.a_scale[r0 + lane] : 0.f;
+        __syncwarp();
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + lane * 4), "f"(as) : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float k[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3]) : "r"(own + i * 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i + j] = __float_as_uint(static_cast<float>(static_cast<int>(v[i + j])) * k[j] * ws);
+        }
+    }
+    if (a.out_dtype == MOE_DTYPE_F32) {
+        float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
+        if (OP == kOpWgrad && a.accumulate) {
+            // each element has one owner: one addition, in no one's order
+#pragma unroll
+            for (int i = 0; i < 32; ++i, o += a.out_stride)
+                if (i < n && f < a.M) red_add_f32(o, __uint_as_float(v[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i, o += a.out_stride)
+                if (i < n && f < a.M) *o = __uint_as_float(v[i]);
+        }
+    } else if (f < a.M) {                         // M is even: both lanes of a pair or neither
+        store_pairs(static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1), a.out_stride, v, n,
+                    a.out_dtype == MOE_DTYPE_F16, f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u);
+    }
+}
+
 template <int OP, bool I8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads<OP>(), 1)
 grouped_tc_kernel(const __grid_constant__ TcArgs a) {
@@ -298,7 +364,8 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     uint64_t* tempty = tfull + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
     int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-    int* s_off = s_abort + 1;
+    int* s_warp = s_abort + 1;                       // [16]: sums of the warps
+    int* s_off = s_warp + 16;
     int* s_base = s_off + a.E + 1;
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -316,15 +383,21 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
         *s_abort = 0;
         fence_mbar_init();
     }
-    const bool sound = load_offsets<OP>(a, s_off, s_base);   // the same in both CTAs
-    if (!sound) {
-        if (tid == 0) atomicOr(&g_grouped_err, kErrBadId);
-        return;
-    }
     if (warp == 1) tmem_alloc_pair(s_tmem, 512);
+    if (warp == 0 && elect_one()) {
+        prefetch_tensormap(&a.tmA);
+        prefetch_tensormap(&a.tmB);
+        if (OP != kOpWgrad) prefetch_tensormap(&a.tmB128);
+    }
+    const bool sound = load_offsets<OP>(a, s_off, s_base, s_warp);   // the same in both CTAs
     tc_fence_before();
     cluster_sync_all();       // the peer's barriers are initialised before any signal
     tc_fence_after();
+    if (!sound) {
+        if (tid == 0) atomicOr(&g_grouped_err, kErrBadId);
+        if (warp == 1) tmem_dealloc_pair(*s_tmem, 512);
+        return;
+    }
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     const uint32_t ring_base = smem_u32(ring);
     const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(full), 0), 0);   // the first CTA's full[0]
@@ -338,11 +411,6 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 
     if (warp == 0) {
         // ------------------------------------------------------ producer
-        if (elect_one()) {
-            prefetch_tensormap(&a.tmA);
-            prefetch_tensormap(&a.tmB);
-        }
-        __syncwarp();
         int s = 0;
         uint32_t phase = 1;                      // a ring that was never filled is free
         int used = 0;                            // stages filled at least once
@@ -479,57 +547,28 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             // columns: tokens, or (wgrad) rows of the expert's dW
             const int valid = OP == kOpWgrad ? min(kTile, a.N - g.n0) : g.valid;
             const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
+            const bool empty_expert = OP == kOpWgrad && g.nk == 0;
+            const bool store = f0 < a.M && !(empty_expert && a.accumulate);
+            uint32_t v[2][32];
+            if (store && part * 32 < valid && !empty_expert) tmem_ld32(taddr + part * 32, v[0]);
 #pragma unroll 1
-            for (int c = part * 32; c < valid && f0 < a.M; c += 64) {
-                uint32_t v[32];
-                if (OP == kOpWgrad && g.nk == 0) {            // an expert without rows
-                    if (a.accumulate) break;
+            for (int c0 = part * 32; store && c0 < valid; c0 += 128) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                } else {
-                    tmem_ld32(taddr + c, v);
-                }
-                const int64_t r0 = col0 + c;
-                const int n = valid - c;                      // columns to store, if below 32
-                if constexpr (I8) {
-                    // the tokens' scales, four to a load from shared memory
-                    const float as = lane < n ? a.a_scale[r0 + lane] : 0.f;
-                    __syncwarp();
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + lane * 4), "f"(as) : "memory");
-                    __syncwarp();
+                for (int j = 0; j < 2; ++j) {                 // this warp's 32 columns of each 64
+                    const int c = c0 + j * 64;
+                    if (c >= valid) break;
                     tmem_ld_wait();
+                    if (c + 64 < valid && !empty_expert) tmem_ld32(taddr + c + 64, v[j ^ 1]);
+                    if (empty_expert) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float k[4];
-                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3]) : "r"(own + i * 4));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[i + j] = __float_as_uint(static_cast<float>(static_cast<int>(v[i + j])) * k[j] * ws);
+                        for (int i = 0; i < 32; ++i) v[j][i] = 0u;
                     }
-                } else {
-                    tmem_ld_wait();
-                }
-                if (a.out_dtype == MOE_DTYPE_F32) {
-                    float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
-                    if (OP == kOpWgrad && a.accumulate) {
-                        // each element has one owner: one addition, in no one's order
-#pragma unroll
-                        for (int i = 0; i < 32; ++i, o += a.out_stride)
-                            if (i < n && f < a.M) red_add_f32(o, __uint_as_float(v[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i, o += a.out_stride)
-                            if (i < n && f < a.M) *o = __uint_as_float(v[i]);
-                    }
-                } else if (f < a.M) {                         // M is even: both lanes of a pair or neither
-                    store_pairs(static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1), a.out_stride, v, n,
-                                a.out_dtype == MOE_DTYPE_F16, f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u);
+                    store_columns<OP, I8>(a, v[j], col0 + c, valid - c, f, f0, ws, own);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_u + b * 8, 0));
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
         }
     } else {
         // wgrad: zeros the rows past a segment's end in its last step, up to
@@ -561,7 +600,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 
 template <int OP>
 size_t tc_smem_bytes(int E) {
-    return 1024 + kStages * kStage + (4 * kStages + 4) * 8 + 8 +
+    return 1024 + kStages * kStage + (4 * kStages + 4) * 8 + 8 + 16 * 4 +
            kEpiBytes + (OP == kOpWgrad ? 0 : 2 * (static_cast<size_t>(E) + 1) * 4);
 }
 
