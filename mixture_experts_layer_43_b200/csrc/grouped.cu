@@ -47,6 +47,12 @@ constexpr int kKBytes = 128;                      // k-step: 64 16-bit or 128 8-
 constexpr int kStageHalf = kHalf * kKBytes;       // 16 KB, of A and of B
 constexpr int kStage = 2 * kStageHalf;
 constexpr int kStages = 6;
+// An fp32 result is summed in segments of this many k-steps (512 terms), which
+// the epilogue adds up: the tensor core cuts its accumulator to fp32 after each
+// 16 terms, always towards zero, which over a long reduction costs more than
+// roundings to nearest (measured over 1024 rows: 1.0e-6 of the result in one
+// sum).  A 16-bit result does not show it.
+constexpr int kSegment = 8;
 constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
 constexpr int kEpiWarps = 8;                      // two for each quarter of the TMEM lanes
 constexpr int kEpiBytes = kEpiWarps * 128;        // 8 bits: 32 scales for each
@@ -308,8 +314,9 @@ __device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const
 }
 
 // 32 accumulator columns (tokens r0 .. of gemm and dgrad, rows of dW in wgrad),
-// n of them if below 32, of this lane's feature f; f0 is lane 0's.
-template <int OP, bool I8>
+// n of them if below 32, of this lane's feature f; f0 is lane 0's.  Results of
+// 16 bits; in 8 bits of fp32, too.
+template <bool I8>
 __device__ __forceinline__ void store_columns(const TcArgs& a, uint32_t (&v)[32], int64_t r0, int n, int f, int f0,
                                               float ws, uint32_t own) {
     const int lane = threadIdx.x & 31;
@@ -329,25 +336,29 @@ __device__ __forceinline__ void store_columns(const TcArgs& a, uint32_t (&v)[32]
                 v[i + j] = __float_as_uint(static_cast<float>(static_cast<int>(v[i + j])) * k[j] * ws);
         }
     }
-    if (a.out_dtype == MOE_DTYPE_F32) {
+    if (I8 && a.out_dtype == MOE_DTYPE_F32) {
         float* o = static_cast<float*>(a.out) + r0 * a.out_stride + f;
-        if (OP == kOpWgrad && a.accumulate) {
-            // each element has one owner: one addition, in no one's order
 #pragma unroll
-            for (int i = 0; i < 32; ++i, o += a.out_stride)
-                if (i < n && f < a.M) red_add_f32(o, __uint_as_float(v[i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i, o += a.out_stride)
-                if (i < n && f < a.M) *o = __uint_as_float(v[i]);
-        }
+        for (int i = 0; i < 32; ++i, o += a.out_stride)
+            if (i < n && f < a.M) *o = __uint_as_float(v[i]);
     } else if (f < a.M) {                         // M is even: both lanes of a pair or neither
         store_pairs(static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1), a.out_stride, v, n,
                     a.out_dtype == MOE_DTYPE_F16, f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u);
     }
 }
 
-template <int OP, bool I8>
+// 16 consecutive fp32 columns of this thread's TMEM lane (warp-wide).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// F32: 16-bit operands with an fp32 result, summed in segments (see kSegment).
+template <int OP, bool I8, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads<OP>(), 1)
 grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     constexpr int kElem = I8 ? 1 : 2;
@@ -488,45 +499,51 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             int s = 0, local = 0;
             uint32_t phase = 0;
             uint32_t pad_phase = 0;                  // a bit for each stage: uses of its padded[]
-            for (; walk.next(g); ++local) {
-                const int b = local & 1;
-                wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
-                tc_fence_after();
-                const uint32_t d_tmem = tmem + b * kTile;
+            while (walk.next(g)) {
                 const uint32_t idesc = a.idesc | (static_cast<uint32_t>(g.cols >> 3) << 17);
-                // wgrad: 16-row slices of the last step, and whether it is padded
-                const int last = OP == kOpWgrad ? (((g.valid - 1) & 63) >> 4) + 1 : 4;
+                // full steps, then (wgrad) a last one of 1 to 4 slices of 16 rows
                 const int n_full = OP == kOpWgrad && (g.valid & 63) ? g.nk - 1 : g.nk;
-                for (int kb = 0; kb < n_full; ++kb) {
-                    wait(full_u + s * 8, phase);
+                int kb = 0;
+                do {                                 // a segment of the reduction
+                    const int b = local & 1;
+                    wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
                     tc_fence_after();
-                    const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
-                    const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
-                    if (elect_one()) {
+                    const uint32_t d_tmem = tmem + b * kTile;
+                    const int end = F32 ? min(kb + kSegment, g.nk) : g.nk, k0 = kb;
+                    for (; kb < min(end, n_full); ++kb) {
+                        wait(full_u + s * 8, phase);
+                        tc_fence_after();
+                        const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
+                        const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk ? 1u : kb != 0);
-                        umma_commit_pair(&empty[s]);
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk ? 1u : kb != k0);
+                            umma_commit_pair(&empty[s]);
+                        }
+                        if (++s == kStages) { s = 0; phase ^= 1; }
                     }
-                    if (++s == kStages) { s = 0; phase ^= 1; }
-                }
-                if (n_full < g.nk) {
-                    wait(full_u + s * 8, phase);
-                    if (g.valid & 15) {
-                        wait(padded_u + s * 8, (pad_phase >> s) & 1);
-                        pad_phase ^= 1u << s;
+                    if (OP == kOpWgrad && kb < end) {
+                        wait(full_u + s * 8, phase);
+                        if (g.valid & 15) {
+                            wait(padded_u + s * 8, (pad_phase >> s) & 1);
+                            pad_phase ^= 1u << s;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
+                        const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
+                        const int slices = (((g.valid - 1) & 63) >> 4) + 1;
+                        if (elect_one()) {
+                            for (int kk = 0; kk < slices; ++kk)
+                                umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk || kb != k0 ? 1u : 0u);
+                            umma_commit_pair(&empty[s]);
+                        }
+                        if (++s == kStages) { s = 0; phase ^= 1; }
+                        ++kb;
                     }
-                    tc_fence_after();
-                    const uint64_t ad = a0 + static_cast<uint32_t>(s * (kStage / 16));
-                    const uint64_t bd = b0 + static_cast<uint32_t>(s * (kStage / 16));
-                    if (elect_one()) {
-                        for (int kk = 0; kk < last; ++kk)
-                            umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk || n_full ? 1u : 0u);
-                        umma_commit_pair(&empty[s]);
-                    }
-                    if (++s == kStages) { s = 0; phase ^= 1; }
-                }
-                if (elect_one()) umma_commit_pair(&tfull[b]);
+                    if (elect_one()) umma_commit_pair(&tfull[b]);
+                    ++local;
+                } while (kb < g.nk);
             }
         }
     } else if (warp < 2 + kEpiWarps) {
@@ -535,12 +552,8 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
         const int part = (warp - 2) >> 2;              // of the quarter's two warps
         const uint32_t own = smem_u32(epi) + (warp - 2) * 128;       // 8 bits: 32 tokens' scales
         int local = 0;
-        for (; walk.next(g); ++local) {
-            // every decision before the warp-collective tcgen05.ld is warp-uniform
-            const int b = local & 1;
-            if (__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1))) continue;
-            tc_fence_after();
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile;
+        while (walk.next(g)) {
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
             const int f0 = g.m0 + kHalf * rank + q * 32;      // this warp's first feature
             const int f = f0 + lane;
             const float ws = I8 && f < a.M ? a.w_scale[static_cast<int64_t>(g.e) * a.M + f] : 1.f;
@@ -548,27 +561,82 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             const int valid = OP == kOpWgrad ? min(kTile, a.N - g.n0) : g.valid;
             const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
             const bool empty_expert = OP == kOpWgrad && g.nk == 0;
-            const bool store = f0 < a.M && !(empty_expert && a.accumulate);
-            uint32_t v[2][32];
-            if (store && part * 32 < valid && !empty_expert) tmem_ld32(taddr + part * 32, v[0]);
-#pragma unroll 1
-            for (int c0 = part * 32; store && c0 < valid; c0 += 128) {
+            bool store = f0 < a.M && !(empty_expert && a.accumulate);
+            if constexpr (F32) {
+                // the segments' sums are added up here, in fp32 rounded to nearest
+                float sum[kTile / 64][32];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {                 // this warp's 32 columns of each 64
-                    const int c = c0 + j * 64;
-                    if (c >= valid) break;
-                    tmem_ld_wait();
-                    if (c + 64 < valid && !empty_expert) tmem_ld32(taddr + c + 64, v[j ^ 1]);
-                    if (empty_expert) {
+                for (int j = 0; j < kTile / 64; ++j)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[j][i] = 0u;
+                    for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
+                const int segments = empty_expert ? 1 : (g.nk + kSegment - 1) / kSegment;
+                for (int seg = 0; seg < segments; ++seg, ++local) {
+                    const int b = local & 1;
+                    // every decision before the warp-collective tcgen05.ld is warp-uniform
+                    if (__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1))) { store = false; continue; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        const int c = part * 32 + j * 64;
+                        if (store && !empty_expert && c < valid) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t v[16];
+                                tmem_ld16(lanes + b * kTile + c + h * 16, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum[j][h * 16 + i] += __uint_as_float(v[i]);
+                            }
+                        }
                     }
-                    store_columns<OP, I8>(a, v[j], col0 + c, valid - c, f, f0, ws, own);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
                 }
+#pragma unroll
+                for (int j = 0; j < kTile / 64; ++j) {
+                    const int c = part * 32 + j * 64, n = valid - c;
+                    if (!store || n <= 0 || f >= a.M) break;
+                    float* o = static_cast<float*>(a.out) + (col0 + c) * a.out_stride + f;
+                    if (OP == kOpWgrad && a.accumulate) {
+                        // each element has one owner: one addition, in no one's order
+#pragma unroll
+                        for (int i = 0; i < 32; ++i, o += a.out_stride)
+                            if (i < n) red_add_f32(o, sum[j][i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i, o += a.out_stride)
+                            if (i < n) *o = sum[j][i];
+                    }
+                }
+            } else {
+                const int b = local & 1;
+                const bool ok = !__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1));
+                ++local;
+                if (!ok) continue;
+                tc_fence_after();
+                const uint32_t taddr = lanes + b * kTile;
+                uint32_t v[2][32];
+                if (store && part * 32 < valid && !empty_expert) tmem_ld32(taddr + part * 32, v[0]);
+#pragma unroll 1
+                for (int c0 = part * 32; store && c0 < valid; c0 += 128) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {             // this warp's 32 columns of each 64
+                        const int c = c0 + j * 64;
+                        if (c >= valid) break;
+                        tmem_ld_wait();
+                        if (c + 64 < valid && !empty_expert) tmem_ld32(taddr + c + 64, v[j ^ 1]);
+                        if (empty_expert) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[j][i] = 0u;
+                        }
+                        store_columns<I8>(a, v[j], col0 + c, valid - c, f, f0, ws, own);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
         }
     } else {
         // wgrad: zeros the rows past a segment's end in its last step, up to
@@ -655,9 +723,9 @@ bool stack_map(CUtensorMap* m, int elem, const void* base, int64_t cols, int64_t
 
 // Once per device: raise the kernels' shared-memory limit and ask how many
 // pairs fit.
-template <int OP, bool I8>
+template <int OP, bool I8, bool F32>
 bool prepare_kernel(int* pairs) {
-    auto* k = grouped_tc_kernel<OP, I8>;
+    auto* k = grouped_tc_kernel<OP, I8, F32>;
     const int smem = static_cast<int>(tc_smem_bytes<OP>(kMaxExperts));
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
     cudaLaunchConfig_t cfg = {};
@@ -680,8 +748,10 @@ int device_pairs() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     int n = g_info[dev].pairs.load(std::memory_order_acquire);
     if (n) return n;
-    if (!prepare_kernel<kOpGemm, false>(&n) || !prepare_kernel<kOpGemm, true>(&n) ||
-        !prepare_kernel<kOpDgrad, false>(&n) || !prepare_kernel<kOpWgrad, false>(&n)) {
+    if (!prepare_kernel<kOpGemm, false, false>(&n) || !prepare_kernel<kOpGemm, false, true>(&n) ||
+        !prepare_kernel<kOpGemm, true, false>(&n) || !prepare_kernel<kOpDgrad, false, false>(&n) ||
+        !prepare_kernel<kOpDgrad, false, true>(&n) || !prepare_kernel<kOpWgrad, false, false>(&n) ||
+        !prepare_kernel<kOpWgrad, false, true>(&n)) {
         cudaGetLastError();
         return 0;
     }
@@ -689,12 +759,12 @@ int device_pairs() {
     return n;
 }
 
-template <int OP, bool I8>
+template <int OP, bool I8, bool F32>
 moe_status_t launch_tc(const TcArgs& a, int64_t tiles, cudaStream_t stream) {
     const int pairs = device_pairs();
     if (!pairs) return MOE_ERR_CUDA;
     const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-    grouped_tc_kernel<OP, I8><<<grid, tc_threads<OP>(), tc_smem_bytes<OP>(a.E), stream>>>(a);
+    grouped_tc_kernel<OP, I8, F32><<<grid, tc_threads<OP>(), tc_smem_bytes<OP>(a.E), stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -794,10 +864,15 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         tiles = static_cast<int64_t>(c.E) * ceil_div(a.M, kTile) * ceil_div(a.N, kTile);
     }
     if (!ok) return MOE_ERR_INVALID_ARG;
-    if (op == kOpGemm) return i8 ? launch_tc<kOpGemm, true>(a, tiles, stream)
-                                 : launch_tc<kOpGemm, false>(a, tiles, stream);
-    if (op == kOpDgrad) return launch_tc<kOpDgrad, false>(a, tiles, stream);
-    return launch_tc<kOpWgrad, false>(a, tiles, stream);
+    if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, stream);
+    if (c.out_dtype == MOE_DTYPE_F32) {
+        if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, stream);
+        if (op == kOpDgrad) return launch_tc<kOpDgrad, false, true>(a, tiles, stream);
+        return launch_tc<kOpWgrad, false, true>(a, tiles, stream);
+    }
+    if (op == kOpGemm) return launch_tc<kOpGemm, false, false>(a, tiles, stream);
+    if (op == kOpDgrad) return launch_tc<kOpDgrad, false, false>(a, tiles, stream);
+    return launch_tc<kOpWgrad, false, false>(a, tiles, stream);
 }
 
 moe_status_t grouped_status_read() {

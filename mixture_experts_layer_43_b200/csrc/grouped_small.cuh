@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
     for (bool more = true; more; cur = next) {
         next = cur;
         more = advance(next);
-        uint32_t c[4] = {0, 0, 0, 0};
+        uint32_t c[4] = {0, 0, 0, 0}, d[4] = {0, 0, 0, 0};    // two sums: half as many cuts to fp32 in each
         int k0 = k_first;
         do {                                           // the loads of the next step, or unit, go ahead of the MMAs
             uint4 cl[4], ch[4], cb[4];
@@ -136,9 +136,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 small_mma<I8>(c, cl[u].x, ch[u].x, cl[u].y, ch[u].y, cb[u].x, cb[u].y, a.f16);
-                small_mma<I8>(c, cl[u].z, ch[u].z, cl[u].w, ch[u].w, cb[u].z, cb[u].w, a.f16);
+                small_mma<I8>(d, cl[u].z, ch[u].z, cl[u].w, ch[u].w, cb[u].z, cb[u].w, a.f16);
             }
         } while (k0 < a.k_bytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = I8 ? c[i] + d[i] : __float_as_uint(__uint_as_float(c[i]) + __uint_as_float(d[i]));
         part[warp][2 * t][g] = c[0];
         part[warp][2 * t + 1][g] = c[1];
         part[warp][2 * t][g + 8] = c[2];
