@@ -69,6 +69,7 @@ struct TcArgs {
     int E;
     int M, N;              // M: output features (wgrad: d_in).  N: wgrad's columns (d_out)
     int nk;                // k-steps of gemm and dgrad
+    int split;             // pairs of a tile (SPLIT)
     int m_block;           // gemm, dgrad: weight tiles of a block (see TileWalk)
     int out_dtype, accumulate;
     uint32_t idesc;        // without the N field
@@ -135,6 +136,13 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+// Arrive on `bar` (the same offset) in the CTAs of the cluster that `ctas` names
+// once every MMA this thread issued so far completes.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t ctas) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar), "h"(ctas) : "memory");
+}
 // Arrive on a barrier of either CTA without waiting for this thread's global
 // stores (which a release at cluster scope would): what it hands over is tensor
 // memory, ordered by the tcgen05 fences.
@@ -170,24 +178,25 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 struct Tile {
     int e, m0, n0, row0, valid;
     int cols;        // MMA N: valid columns rounded up to 32
-    int nk;
+    int nk;          // k-steps of the tile
+    int k_from, k_to;  // ... and of this pair
 };
 
 // Walks the tile numbers first, first + step, ...: expert by expert; within an
 // expert of gemm and dgrad by blocks of m_block weight tiles, and within a block
 // by row chunks, so that the block's weights stay in L2 while the rows stream by
 // once for each block.
-template <int OP>
+template <int OP, bool SPLIT>
 struct TileWalk {
     const TcArgs& a;
     const int* off;        // in shared memory (wgrad: the caller's table)
     const int* base;       // gemm, dgrad: row chunks of the experts before e
     int mt, nt;
     int64_t t, total;
-    int step, e = 0;
+    int step, pair, e = 0;
 
-    __device__ TileWalk(const TcArgs& args, const int* s_off, const int* s_base, int first, int n)
-        : a(args), off(s_off), base(s_base), t(first), step(n) {
+    __device__ TileWalk(const TcArgs& args, const int* s_off, const int* s_base, int first, int n, int of_tile)
+        : a(args), off(s_off), base(s_base), t(first), step(n), pair(of_tile) {
         mt = (a.M + kTile - 1) / kTile;
         nt = OP == kOpWgrad ? (a.N + kTile - 1) / kTile : 0;
         total = OP == kOpWgrad ? static_cast<int64_t>(a.E) * mt * nt
@@ -229,6 +238,13 @@ struct TileWalk {
             g.cols = (g.valid + 31) & ~31;
             g.nk = a.nk;
         }
+        g.k_from = 0;
+        g.k_to = g.nk;
+        if (SPLIT) {
+            const int per = (g.nk + a.split - 1) / a.split;
+            g.k_from = min(g.nk, pair * per);
+            g.k_to = min(g.nk, g.k_from + per);
+        }
         t += step;
         return true;
     }
@@ -259,29 +275,29 @@ __device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base, int* s_wa
         }
         sum += count[i];
     }
-    if (OP == kOpWgrad) {
+    if constexpr (OP == kOpWgrad) {
         bad = __syncthreads_or(bad);
-        return !bad;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (e0 + i <= a.E) s_off[e0 + i] = v[i];
-    if (a.E == kMaxExperts && e0 + kPer == a.E) s_off[a.E] = v[kPer];
-    int upto = sum;
+        for (int i = 0; i < kPer; ++i)
+            if (e0 + i <= a.E) s_off[e0 + i] = v[i];
+        if (a.E == kMaxExperts && e0 + kPer == a.E) s_off[a.E] = v[kPer];
+        int upto = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += o;
-    }
-    if (lane == 31) s_warp[warp] = upto;
-    bad = __syncthreads_or(bad);
-    int before = upto - sum;
-    for (int w = 0; w < warp; ++w) before += s_warp[w];
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) s_warp[warp] = upto;
+        bad = __syncthreads_or(bad);
+        int before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += s_warp[w];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (e0 + i < a.E) s_base[e0 + i] = before;
-        before += count[i];
-        if (e0 + i == a.E - 1) s_base[a.E] = before;
+        for (int i = 0; i < kPer; ++i) {
+            if (e0 + i < a.E) s_base[e0 + i] = before;
+            before += count[i];
+            if (e0 + i == a.E - 1) s_base[a.E] = before;
+        }
     }
     return !bad;
 }
@@ -358,8 +374,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 
 // F32: 16-bit operands with an fp32 result, summed in segments (see kSegment).
-template <int OP, bool I8, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tc_threads<OP>(), 1)
+// SPLIT: a.split pairs (a cluster of 2 a.split CTAs, one tile each) take parts
+// of a tile's reduction and trade their sums through distributed shared memory,
+// each adding up (in a fixed order) and storing its share of the columns.
+template <int OP, bool I8, bool F32, bool SPLIT>
+__global__ void __launch_bounds__(tc_threads<OP>(), 1)
 grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     constexpr int kElem = I8 ? 1 : 2;
     constexpr int kBK = kKBytes / kElem;
@@ -381,8 +400,12 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);      // the same in every lane, and known to be
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int unit = static_cast<int>(blockIdx.x) / 2, n_units = static_cast<int>(gridDim.x) / 2;
+    const int cta = static_cast<int>(cluster_ctarank());
+    const int rank = SPLIT ? cta & 1 : cta;                      // in the pair
+    const int pair = SPLIT ? cta >> 1 : 0;
+    const int leader = cta - rank;                               // the pair's first CTA
+    const int unit = static_cast<int>(blockIdx.x) / (SPLIT ? 2 * a.split : 2);
+    const int n_units = static_cast<int>(gridDim.x) / (SPLIT ? 2 * a.split : 2);
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -411,13 +434,14 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     }
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     const uint32_t ring_base = smem_u32(ring);
-    const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(full), 0), 0);   // the first CTA's full[0]
-    const uint32_t landed0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(landed), rank), 0);
+    const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(full), leader), 0);   // the first CTA's full[0]
+    const uint32_t landed0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(landed), cta), 0);
+    const uint16_t both = static_cast<uint16_t>(3u << leader);
     volatile int* abort_flag = s_abort;
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_cluster(bar, parity, abort_flag); };
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed);
     const uint32_t padded_u = smem_u32(padded), tfull_u = smem_u32(tfull), tempty_u = smem_u32(tempty);
-    TileWalk<OP> walk(a, OP == kOpWgrad ? a.offsets : s_off, s_base, unit, n_units);
+    TileWalk<OP, SPLIT> walk(a, OP == kOpWgrad ? a.offsets : s_off, s_base, unit, n_units, pair);
     Tile g;
 
     if (warp == 0) {
@@ -435,7 +459,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             const int nb = OP == kOpWgrad ? (half + 63) / 64 : big ? 4 : (half + kBoxRows - 1) / kBoxRows;
             const uint32_t bytes = kStageHalf + nb * (OP == kOpWgrad ? 8192u : kBoxRows * kKBytes);
             const int r0 = OP == kOpWgrad ? g.row0 : g.row0 + half * rank;
-            for (int kb = 0; kb < g.nk; ++kb) {
+            for (int kb = g.k_from; kb < g.k_to; ++kb) {
                 stop |= !wait(empty_u + s * 8, phase);
                 const uint32_t A = ring_base + s * kStage;
                 const uint32_t B = A + kStageHalf;
@@ -503,13 +527,13 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                 const uint32_t idesc = a.idesc | (static_cast<uint32_t>(g.cols >> 3) << 17);
                 // full steps, then (wgrad) a last one of 1 to 4 slices of 16 rows
                 const int n_full = OP == kOpWgrad && (g.valid & 63) ? g.nk - 1 : g.nk;
-                int kb = 0;
+                int kb = g.k_from;
                 do {                                 // a segment of the reduction
                     const int b = local & 1;
                     wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + b * kTile;
-                    const int end = F32 ? min(kb + kSegment, g.nk) : g.nk, k0 = kb;
+                    const int end = F32 ? min(kb + kSegment, g.k_to) : g.k_to, k0 = kb;
                     for (; kb < min(end, n_full); ++kb) {
                         wait(full_u + s * 8, phase);
                         tc_fence_after();
@@ -519,7 +543,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk ? 1u : kb != k0);
-                            umma_commit_pair(&empty[s]);
+                            commit_pair(empty_u + s * 8, both);
                         }
                         if (++s == kStages) { s = 0; phase ^= 1; }
                     }
@@ -536,14 +560,14 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                         if (elect_one()) {
                             for (int kk = 0; kk < slices; ++kk)
                                 umma_pair<I8>(d_tmem, ad + kk * kStepA, bd + kk * kStepB, idesc, kk || kb != k0 ? 1u : 0u);
-                            umma_commit_pair(&empty[s]);
+                            commit_pair(empty_u + s * 8, both);
                         }
                         if (++s == kStages) { s = 0; phase ^= 1; }
                         ++kb;
                     }
-                    if (elect_one()) umma_commit_pair(&tfull[b]);
+                    if (elect_one()) commit_pair(tfull_u + b * 8, both);
                     ++local;
-                } while (kb < g.nk);
+                } while (kb < g.k_to);
             }
         }
     } else if (warp < 2 + kEpiWarps) {
@@ -562,14 +586,16 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
             const bool empty_expert = OP == kOpWgrad && g.nk == 0;
             bool store = f0 < a.M && !(empty_expert && a.accumulate);
-            if constexpr (F32) {
+            if constexpr (F32 || SPLIT) {
                 // the segments' sums are added up here, in fp32 rounded to nearest
+                // (8 bits: one segment, whose words are int32)
                 float sum[kTile / 64][32];
 #pragma unroll
                 for (int j = 0; j < kTile / 64; ++j)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
-                const int segments = empty_expert ? 1 : (g.nk + kSegment - 1) / kSegment;
+                const bool none = g.k_from == g.k_to;
+                const int segments = F32 && !none ? (g.k_to - g.k_from + kSegment - 1) / kSegment : 1;
                 for (int seg = 0; seg < segments; ++seg, ++local) {
                     const int b = local & 1;
                     // every decision before the warp-collective tcgen05.ld is warp-uniform
@@ -578,35 +604,78 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 #pragma unroll
                     for (int j = 0; j < kTile / 64; ++j) {
                         const int c = part * 32 + j * 64;
-                        if (store && !empty_expert && c < valid) {
+                        if (store && !none && c < valid) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t v[16];
                                 tmem_ld16(lanes + b * kTile + c + h * 16, v);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[j][h * 16 + i] += __uint_as_float(v[i]);
+                                for (int i = 0; i < 16; ++i)
+                                    sum[j][h * 16 + i] = F32 ? sum[j][h * 16 + i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
                             }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
+                    if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, leader));
+                }
+                // SPLIT: group k of 32 columns is pair k mod split's, who gets the
+                // others' sums of it as [other pair][its group][column][128 rows] in its
+                // ring, which no load or MMA of the cluster uses after this barrier
+                const int groups = SPLIT ? (g.cols / 32 + a.split - 1) / a.split : 0;      // of a pair, at most
+                const int mine = (q * 32 + lane) * 4;
+                if constexpr (SPLIT) {
+                    cluster_sync_all();
+#pragma unroll
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        const int k = part + 2 * j, owner = k & (a.split - 1);
+                        if (!store || k * 32 >= valid) break;
+                        if (owner == pair) continue;
+                        const int from = pair < owner ? pair : pair - 1;
+                        const uint32_t to = mapa_shared(ring_base, owner * 2 + rank) + mine +
+                                            (from * groups + k / a.split) * (32 * 512);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 512), "f"(sum[j][i]) : "memory");
+                    }
+                    cluster_sync_all();
                 }
 #pragma unroll
                 for (int j = 0; j < kTile / 64; ++j) {
-                    const int c = part * 32 + j * 64, n = valid - c;
-                    if (!store || n <= 0 || f >= a.M) break;
-                    float* o = static_cast<float*>(a.out) + (col0 + c) * a.out_stride + f;
-                    if (OP == kOpWgrad && a.accumulate) {
-                        // each element has one owner: one addition, in no one's order
+                    const int k = part + 2 * j, c = k * 32, n = valid - c;
+                    if (!store || n <= 0) break;
+                    if constexpr (SPLIT) {
+                        if ((k & (a.split - 1)) != pair) continue;
+                        for (int from = 0; from < a.split - 1; ++from) {
+                            const uint8_t* at = ring + mine + (from * groups + k / a.split) * (32 * 512);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i, o += a.out_stride)
-                            if (i < n) red_add_f32(o, sum[j][i]);
+                            for (int h = 0; h < 32; h += 16) {          // 16 loads in flight
+                                float o[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = *reinterpret_cast<const volatile float*>(at + (h + i) * 512);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[j][h + i] = I8 ? __int_as_float(__float_as_int(sum[j][h + i]) + __float_as_int(o[i]))
+                                                       : sum[j][h + i] + o[i];
+                            }
+                        }
+                    }
+                    if constexpr (F32) {
+                        if (f >= a.M) break;
+                        float* o = static_cast<float*>(a.out) + (col0 + c) * a.out_stride + f;
+                        if (OP == kOpWgrad && a.accumulate) {
+                            // each element has one owner: one addition, in no one's order
+#pragma unroll
+                            for (int i = 0; i < 32; ++i, o += a.out_stride)
+                                if (i < n) red_add_f32(o, sum[j][i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i, o += a.out_stride)
+                                if (i < n) *o = sum[j][i];
+                        }
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i, o += a.out_stride)
-                            if (i < n) *o = sum[j][i];
+                        store_columns<I8>(a, reinterpret_cast<uint32_t (&)[32]>(sum[j]), col0 + c, n, f, f0, ws, own);
                     }
                 }
             } else {
@@ -635,7 +704,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, 0));
+                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, leader));
             }
         }
     } else {
@@ -643,9 +712,9 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
         // the next multiple of the MMA's 16, once this CTA's loads have landed
         uint32_t it = 0, phase = 0;
         while (walk.next(g)) {
-            it += g.nk;
+            it += g.k_to - g.k_from;
             const int pad = -g.valid & 15;
-            if (pad == 0 || g.nk == 0) continue;
+            if (pad == 0 || g.k_to != g.nk || g.k_from == g.k_to) continue;
             const int s = (it - 1) % kStages;
             if (__any_sync(0xffffffffu, !wait(landed_u + s * 8, (phase >> s) & 1))) break;
             phase ^= 1u << s;
@@ -656,8 +725,15 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(padded_u + s * 8, 0));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(padded_u + s * 8, leader));
         }
+    }
+    if (SPLIT && !(warp >= 2 && warp < 2 + kEpiWarps && walk.t != unit)) {
+        // the epilogue's two barriers, for the warps that have no part in it (and
+        // for all where the cluster has no tile)
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
     }
     tc_fence_before();
     __syncwarp();
@@ -723,11 +799,13 @@ bool stack_map(CUtensorMap* m, int elem, const void* base, int64_t cols, int64_t
 
 // Once per device: raise the kernels' shared-memory limit and ask how many
 // pairs fit.
-template <int OP, bool I8, bool F32>
+template <int OP, bool I8, bool F32, bool SPLIT>
 bool prepare_kernel(int* pairs) {
-    auto* k = grouped_tc_kernel<OP, I8, F32>;
+    auto* k = grouped_tc_kernel<OP, I8, F32, SPLIT>;
     const int smem = static_cast<int>(tc_smem_bytes<OP>(kMaxExperts));
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    // clusters of 8 are within the portable size: nothing more to ask for
+    if (SPLIT) return true;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(tc_threads<OP>());
@@ -743,15 +821,20 @@ bool prepare_kernel(int* pairs) {
     return true;
 }
 
+template <int OP, bool I8, bool F32>
+bool prepare_kernels(int* pairs) {
+    return prepare_kernel<OP, I8, F32, false>(pairs) && prepare_kernel<OP, I8, F32, true>(pairs);
+}
+
 int device_pairs() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     int n = g_info[dev].pairs.load(std::memory_order_acquire);
     if (n) return n;
-    if (!prepare_kernel<kOpGemm, false, false>(&n) || !prepare_kernel<kOpGemm, false, true>(&n) ||
-        !prepare_kernel<kOpGemm, true, false>(&n) || !prepare_kernel<kOpDgrad, false, false>(&n) ||
-        !prepare_kernel<kOpDgrad, false, true>(&n) || !prepare_kernel<kOpWgrad, false, false>(&n) ||
-        !prepare_kernel<kOpWgrad, false, true>(&n)) {
+    if (!prepare_kernels<kOpGemm, false, false>(&n) || !prepare_kernels<kOpGemm, false, true>(&n) ||
+        !prepare_kernels<kOpGemm, true, false>(&n) || !prepare_kernels<kOpDgrad, false, false>(&n) ||
+        !prepare_kernels<kOpDgrad, false, true>(&n) || !prepare_kernels<kOpWgrad, false, false>(&n) ||
+        !prepare_kernels<kOpWgrad, false, true>(&n)) {
         cudaGetLastError();
         return 0;
     }
@@ -759,16 +842,40 @@ int device_pairs() {
     return n;
 }
 
-template <int OP, bool I8, bool F32>
-moe_status_t launch_tc(const TcArgs& a, int64_t tiles, cudaStream_t stream) {
-    const int pairs = device_pairs();
-    if (!pairs) return MOE_ERR_CUDA;
-    const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-    grouped_tc_kernel<OP, I8, F32><<<grid, tc_threads<OP>(), tc_smem_bytes<OP>(a.E), stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Pairs that share a tile's reduction.  With so few tiles that most SMs would
+// idle, two or four pairs to a tile share its loads (an SM fills its shared
+// memory at about 100 GB/s) for some 3 us of trading sums.  Measured, 1 / 2 / 4
+// pairs: 64 rows through 4096 x 1024 (4 tiles, 64 k-steps) 19.5 / 14.4 / 11.6 us,
+// 4096 x 3328 (13 tiles) 19.7 / 14.4 / 12.1, 4096 x 4096 (16) 19.7 / 14.9 / 22.3 (not
+// all of its 8-CTA clusters fit at once), 2048 x 8192 (32 tiles, 32 steps) 12.8 / 11.8
+// / 27.6, 1024 x 1024 (16 steps) 8.9 / 9.3 / 8.9; with more than 128 columns to
+// trade, a weight gradient of 24 steps and 12 tiles 13.9 / 14.0 / 14.4.
+int pick_split(int64_t tiles, int nk, int cols) {
+    if (nk < (cols > 128 ? 32 : 24)) return 1;
+    return tiles <= 13 ? 4 : tiles <= 32 ? 2 : 1;
 }
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+template <int OP, bool I8, bool F32>
+moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t stream) {
+    const int pairs = device_pairs();
+    if (!pairs) return MOE_ERR_CUDA;
+    a.split = pick_split(tiles, nk, cols);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(a.split > 1 ? tiles * a.split : tiles < pairs ? tiles : pairs));
+    cfg.blockDim = dim3(tc_threads<OP>());
+    cfg.dynamicSmemBytes = tc_smem_bytes<OP>(a.E);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * a.split; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.split > 1 ? cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, I8, F32, true>, a)
+                                      : cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, I8, F32, false>, a);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
 
 // Whether a product goes to grouped_small_kernel: its 256-row weight tiles keep
 // at most half of the CTA pairs busy, and its experts average at most 16 rows
@@ -836,7 +943,9 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         const int64_t mb = (32 << 20) / (kTile * k_bytes);
         a.m_block = static_cast<int>(mb < 1 ? 1 : mb > 64 ? 64 : mb);
     }
-    const int64_t chunks = ceil_div(c.rows, kTile) + (c.rows < c.E ? c.rows : c.E);   // at most
+    // at most so many row chunks: each expert with rows adds at most 255 of padding
+    const int64_t chunks = (c.rows + 255 * (c.rows < c.E ? c.rows : c.E)) / kTile;
+    int nk, cols = c.rows < kTile ? static_cast<int>(c.rows) : kTile;      // of a tile, at most
     if (op == kOpGemm) {
         a.M = c.d_out;
         a.nk = static_cast<int>(ceil_div(c.d_in, bk));
@@ -845,6 +954,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         ok &= rows_map(&a.tmB, elem, c.a, c.d_in, c.rows, c.x_stride, bk, kBoxRows);
         ok &= rows_map(&a.tmB128, elem, c.a, c.d_in, c.rows, c.x_stride, bk, 128);
         tiles = chunks * ceil_div(a.M, kTile);
+        nk = a.nk;
     } else if (op == kOpDgrad) {
         a.M = c.d_in;
         a.nk = static_cast<int>(ceil_div(c.d_out, bk));
@@ -854,6 +964,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         ok &= rows_map(&a.tmB, elem, c.a, c.d_out, c.rows, c.y_stride, bk, kBoxRows);
         ok &= rows_map(&a.tmB128, elem, c.a, c.d_out, c.rows, c.y_stride, bk, 128);
         tiles = chunks * ceil_div(a.M, kTile);
+        nk = a.nk;
     } else {
         a.M = c.d_in;
         a.N = c.d_out;
@@ -862,17 +973,20 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         ok &= rows_map(&a.tmA, elem, c.w, c.d_in, c.rows, c.x_stride, 64, 64);
         ok &= rows_map(&a.tmB, elem, c.a, c.d_out, c.rows, c.y_stride, 64, 64);
         tiles = static_cast<int64_t>(c.E) * ceil_div(a.M, kTile) * ceil_div(a.N, kTile);
+        nk = static_cast<int>(ceil_div(c.rows, 64 * static_cast<int64_t>(c.E)));            // on average
+        cols = a.N < kTile ? a.N : kTile;
+
     }
     if (!ok) return MOE_ERR_INVALID_ARG;
-    if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, stream);
+    if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, nk, cols, stream);
     if (c.out_dtype == MOE_DTYPE_F32) {
-        if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, stream);
-        if (op == kOpDgrad) return launch_tc<kOpDgrad, false, true>(a, tiles, stream);
-        return launch_tc<kOpWgrad, false, true>(a, tiles, stream);
+        if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, nk, cols, stream);
+        if (op == kOpDgrad) return launch_tc<kOpDgrad, false, true>(a, tiles, nk, cols, stream);
+        return launch_tc<kOpWgrad, false, true>(a, tiles, nk, cols, stream);
     }
-    if (op == kOpGemm) return launch_tc<kOpGemm, false, false>(a, tiles, stream);
-    if (op == kOpDgrad) return launch_tc<kOpDgrad, false, false>(a, tiles, stream);
-    return launch_tc<kOpWgrad, false, false>(a, tiles, stream);
+    if (op == kOpGemm) return launch_tc<kOpGemm, false, false>(a, tiles, nk, cols, stream);
+    if (op == kOpDgrad) return launch_tc<kOpDgrad, false, false>(a, tiles, nk, cols, stream);
+    return launch_tc<kOpWgrad, false, false>(a, tiles, nk, cols, stream);
 }
 
 moe_status_t grouped_status_read() {

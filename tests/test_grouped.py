@@ -204,13 +204,39 @@ def test_wgrad(counts, d_in, d_out, kw, dtype, out, acc):
     check_wgrad(Group(counts, d_in, d_out, dtype, **kw), out, acc)
 
 
+# few weight tiles and a long reduction: several CTA pairs share a tile (1 to 8 groups of 32 columns, one and two
+# tiles, ends inside a k-step), beside the same sizes with a row or two, which go another way
+LONG = [
+    ([40], 4096, 520, dict(behind=3, pad_x=8, pad_y=8)),
+    ([130, 0, 70], 2056, 264, dict(before=2)),
+    ([256], 3080, 1032, {}),
+    ([1, 300], 1544, 8, {}),
+    ([17], 2048, 3336, {}),
+    ([3], 4104, 24, {}),
+]
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("counts,d_in,d_out,kw", LONG, ids=lambda v: str(v)[:24])
+def test_long_reductions_over_few_tiles(counts, d_in, d_out, kw, dtype, out):
+    check_gemm(Group(counts, d_in, d_out, dtype, **kw), out)
+    check_dgrad(Group(counts, d_out, d_in, dtype, **kw), out)
+
+
+@pytest.mark.parametrize("dtype,out,acc", [("bf16", "bf16", False), ("f16", "f32", False), ("bf16", "f32", True)])
+@pytest.mark.parametrize("counts,d_in,d_out", [([2100], 64, 40), ([4099, 0], 264, 520), ([5, 0, 6001], 136, 248),
+                                               ([2500, 2500], 512, 256)], ids=str)
+def test_wgrad_of_many_rows_over_few_tiles(counts, d_in, d_out, dtype, out, acc):
+    check_wgrad(Group(counts, d_in, d_out, dtype, before=1, behind=70), out, acc)
+
+
 def _codes(G, shape):
     return torch.randint(-128, 128, shape, generator=G.gen, device="cuda", dtype=torch.int32).to(torch.int8)
 
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("counts,d_in,d_out,kw", [(c, max(16, d_in // 16 * 16), o, {**k, **({"pad_x": 16} if "pad_x" in k else {})})
-                                                  for c, d_in, o, k in CASES], ids=lambda v: str(v)[:24])
+                                                  for c, d_in, o, k in CASES + LONG], ids=lambda v: str(v)[:24])
 def test_i8_gemm(counts, d_in, d_out, kw, out):
     G = Group(counts, d_in, d_out, "bf16", **kw)
     q = _codes(G, (G.rows, d_in + G.pad["x"]))
