@@ -192,22 +192,21 @@ struct TileWalk {
     const int* off;        // in shared memory (wgrad: the caller's table)
     const int* base;       // gemm, dgrad: row chunks of the experts before e
     int mt, nt;
-    int64_t t, total;
+    int t, total;          // fits: the launch checks it
     int step, pair, e = 0;
 
     __device__ TileWalk(const TcArgs& args, const int* s_off, const int* s_base, int first, int n, int of_tile)
         : a(args), off(s_off), base(s_base), t(first), step(n), pair(of_tile) {
         mt = (a.M + kTile - 1) / kTile;
         nt = OP == kOpWgrad ? (a.N + kTile - 1) / kTile : 0;
-        total = OP == kOpWgrad ? static_cast<int64_t>(a.E) * mt * nt
-                               : static_cast<int64_t>(base[a.E]) * mt;
+        total = OP == kOpWgrad ? a.E * mt * nt : base[a.E] * mt;
     }
     __device__ bool next(Tile& g) {
         if (t >= total) return false;
         if constexpr (OP == kOpWgrad) {
             const int per = mt * nt;
-            g.e = static_cast<int>(t / per);
-            const int r = static_cast<int>(t - static_cast<int64_t>(g.e) * per);
+            g.e = t / per;
+            const int r = t - g.e * per;
             // the shorter side varies fastest: its operand is what L2 keeps
             g.m0 = (mt < nt ? r % mt : r / nt) * kTile;
             g.n0 = (mt < nt ? r / mt : r % nt) * kTile;
@@ -216,22 +215,30 @@ struct TileWalk {
             g.cols = (min(kTile, a.N - g.n0) + 31) & ~31;
             g.nk = (g.valid + 63) / 64;
         } else {
-            int hi = a.E;                       // the last expert whose tiles start at or before t
+            // the last expert whose tiles start at or before t, not far from the last one
+            int hi = e + 1;
+            for (int leap = 1; hi < a.E && base[hi] * mt <= t; leap *= 2) {
+                e = hi;
+                hi = min(a.E, hi + leap);
+            }
             while (hi - e > 1) {
                 const int mid = (e + hi) >> 1;
-                if (static_cast<int64_t>(base[mid]) * mt <= t) e = mid; else hi = mid;
+                if (base[mid] * mt <= t) e = mid; else hi = mid;
             }
             const int c0 = base[e], chunks = base[e + 1] - c0;
-            const int64_t r = t - static_cast<int64_t>(c0) * mt;
-            const int per_block = chunks * a.m_block;
-            const int block = static_cast<int>(r / per_block);
-            const int in_block = static_cast<int>(r - static_cast<int64_t>(block) * per_block);
-            const int mb = min(a.m_block, mt - block * a.m_block);
-            const int ci = in_block / mb;
             const int n = off[e + 1] - off[e];
-            const int per = ((n + chunks - 1) / chunks + 31) & ~31;
+            const int r = t - c0 * mt;
+            int mi = r, ci = 0, per = (n + 31) & ~31;
+            if (chunks > 1) {
+                const int per_block = chunks * a.m_block;
+                const int block = r / per_block, in_block = r - block * per_block;
+                const int mb = min(a.m_block, mt - block * a.m_block);
+                ci = in_block / mb;
+                mi = block * a.m_block + in_block - ci * mb;
+                per = ((n + chunks - 1) / chunks + 31) & ~31;
+            }
             g.e = e;
-            g.m0 = (block * a.m_block + in_block % mb) * kTile;
+            g.m0 = mi * kTile;
             g.n0 = 0;
             g.row0 = off[e] + ci * per;
             g.valid = min(per, n - ci * per);
@@ -306,14 +313,17 @@ __device__ bool load_offsets(const TcArgs& a, int* s_off, int* s_base, int* s_wa
 // 32 columns (tokens) of this lane's feature as 16-bit values, `n` of them
 // stored: even and odd lanes trade half of their packed pairs of tokens, so
 // that each holds two features (4 bytes) of 16 tokens.
+template <bool FULL>
 __device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const uint32_t (&v)[32], int n, bool f16,
                                             uint32_t lanes) {
     const int odd = threadIdx.x & 1;
     const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
+    const int most = n;                            // the same in every lane
     out += odd * 2 * stride;
     n -= odd * 2;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
+        if (!FULL && i >= most) break;
         uint32_t p[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -323,8 +333,8 @@ __device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const
         // an even lane keeps tokens i, i + 1 and an odd one i + 2, i + 3, of both features
         const uint32_t got = __shfl_xor_sync(lanes, odd ? p[0] : p[1], 1);
         const uint32_t keep = odd ? p[1] : p[0];
-        if (i < n) *reinterpret_cast<uint32_t*>(out) = __byte_perm(keep, got, sel_lo);
-        if (i + 1 < n) *reinterpret_cast<uint32_t*>(out + stride) = __byte_perm(keep, got, sel_hi);
+        if (FULL || i < n) *reinterpret_cast<uint32_t*>(out) = __byte_perm(keep, got, sel_lo);
+        if (FULL || i + 1 < n) *reinterpret_cast<uint32_t*>(out + stride) = __byte_perm(keep, got, sel_hi);
         out += 4 * stride;
     }
 }
@@ -334,16 +344,16 @@ __device__ __forceinline__ void store_pairs(uint16_t* out, int64_t stride, const
 // 16 bits; in 8 bits of fp32, too.
 template <bool I8>
 __device__ __forceinline__ void store_columns(const TcArgs& a, uint32_t (&v)[32], int64_t r0, int n, int f, int f0,
-                                              float ws, uint32_t own) {
+                                              float ws, float as, uint32_t own) {
     const int lane = threadIdx.x & 31;
     if constexpr (I8) {
-        // the tokens' scales, four to a load from shared memory
-        const float as = lane < n ? a.a_scale[r0 + lane] : 0.f;
+        // the tokens' scales (as: of token r0 + lane), four to a load from shared memory
         __syncwarp();
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + lane * 4), "f"(as) : "memory");
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
+            if (i >= n) break;
             float k[4];
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3]) : "r"(own + i * 4));
@@ -358,8 +368,11 @@ __device__ __forceinline__ void store_columns(const TcArgs& a, uint32_t (&v)[32]
         for (int i = 0; i < 32; ++i, o += a.out_stride)
             if (i < n && f < a.M) *o = __uint_as_float(v[i]);
     } else if (f < a.M) {                         // M is even: both lanes of a pair or neither
-        store_pairs(static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1), a.out_stride, v, n,
-                    a.out_dtype == MOE_DTYPE_F16, f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u);
+        uint16_t* out = static_cast<uint16_t*>(a.out) + r0 * a.out_stride + (f & ~1);
+        const bool f16 = a.out_dtype == MOE_DTYPE_F16;
+        const uint32_t lanes = f0 + 32 <= a.M ? 0xffffffffu : (1u << (a.M - f0)) - 1u;
+        if (n >= 32) store_pairs<true>(out, a.out_stride, v, n, f16, lanes);
+        else store_pairs<false>(out, a.out_stride, v, n, f16, lanes);
     }
 }
 
@@ -573,7 +586,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     } else if (warp < 2 + kEpiWarps) {
         // ----------------------------------------------------- epilogue
         const int q = warp & 3;                        // TMEM lane quarter of this warp
-        const int part = (warp - 2) >> 2;              // of the quarter's two warps
+        const int first_part = (warp - 2) >> 2;        // of the quarter's two warps
         const uint32_t own = smem_u32(epi) + (warp - 2) * 128;       // 8 bits: 32 tokens' scales
         int local = 0;
         while (walk.next(g)) {
@@ -586,9 +599,13 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
             const bool empty_expert = OP == kOpWgrad && g.nk == 0;
             bool store = f0 < a.M && !(empty_expert && a.accumulate);
+            auto scale_of = [&](int c) {                      // 8 bits: of this lane's token of column c ..
+                return I8 && c + lane < valid ? a.a_scale[col0 + c + lane] : 0.f;
+            };
             if constexpr (F32 || SPLIT) {
                 // the segments' sums are added up here, in fp32 rounded to nearest
                 // (8 bits: one segment, whose words are int32)
+                const int part = first_part;
                 float sum[kTile / 64][32];
 #pragma unroll
                 for (int j = 0; j < kTile / 64; ++j)
@@ -675,11 +692,15 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                                 if (i < n) *o = sum[j][i];
                         }
                     } else {
-                        store_columns<I8>(a, reinterpret_cast<uint32_t (&)[32]>(sum[j]), col0 + c, n, f, f0, ws, own);
+                        store_columns<I8>(a, reinterpret_cast<uint32_t (&)[32]>(sum[j]), col0 + c, n, f, f0, ws, scale_of(c), own);
                     }
                 }
             } else {
                 const int b = local & 1;
+                // the two warps of a quarter take turns at the first 32 columns, so that
+                // tiles of few rows pass through both
+                const int part = first_part ^ b;
+                float as = scale_of(part * 32);
                 const bool ok = !__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1));
                 ++local;
                 if (!ok) continue;
@@ -695,11 +716,13 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                         if (c >= valid) break;
                         tmem_ld_wait();
                         if (c + 64 < valid && !empty_expert) tmem_ld32(taddr + c + 64, v[j ^ 1]);
+                        const float next_as = scale_of(c + 64);
                         if (empty_expert) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[j][i] = 0u;
                         }
-                        store_columns<I8>(a, v[j], col0 + c, valid - c, f, f0, ws, own);
+                        store_columns<I8>(a, v[j], col0 + c, valid - c, f, f0, ws, as, own);
+                        as = next_as;
                     }
                 }
                 tc_fence_before();
@@ -977,7 +1000,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         cols = a.N < kTile ? a.N : kTile;
 
     }
-    if (!ok) return MOE_ERR_INVALID_ARG;
+    if (!ok || tiles > 0x7FFFFFFF) return MOE_ERR_INVALID_ARG;
     if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, nk, cols, stream);
     if (c.out_dtype == MOE_DTYPE_F32) {
         if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, nk, cols, stream);
