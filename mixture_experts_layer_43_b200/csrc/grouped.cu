@@ -436,6 +436,8 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
         prefetch_tensormap(&a.tmB);
         if (OP != kOpWgrad) prefetch_tensormap(&a.tmB128);
     }
+    grid_let_next();
+    grid_wait();
     const bool sound = load_offsets<OP>(a, s_off, s_base, s_warp);   // the same in both CTAs
     tc_fence_before();
     cluster_sync_all();       // the peer's barriers are initialised before any signal
@@ -885,18 +887,11 @@ moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t 
     const int pairs = device_pairs();
     if (!pairs) return MOE_ERR_CUDA;
     a.split = pick_split(tiles, nk, cols);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * static_cast<unsigned>(a.split > 1 ? tiles * a.split : tiles < pairs ? tiles : pairs));
-    cfg.blockDim = dim3(tc_threads<OP>());
-    cfg.dynamicSmemBytes = tc_smem_bytes<OP>(a.E);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * a.split; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = a.split > 1 ? cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, I8, F32, true>, a)
-                                      : cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, I8, F32, false>, a);
+    const dim3 grid(2 * static_cast<unsigned>(a.split > 1 ? tiles * a.split : tiles < pairs ? tiles : pairs));
+    const size_t smem = tc_smem_bytes<OP>(a.E);
+    const cudaError_t e =
+        a.split > 1 ? launch_chained(grouped_tc_kernel<OP, I8, F32, true>, grid, tc_threads<OP>(), smem, 2 * a.split, stream, a)
+                    : launch_chained(grouped_tc_kernel<OP, I8, F32, false>, grid, tc_threads<OP>(), smem, 2, stream, a);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -941,9 +936,9 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         m.out_dtype = c.out_dtype;
         const int64_t units = ceil_div(c.d_out, kSmallRows) * (c.rows < c.E ? c.rows : c.E);    // at most
         const unsigned grid = static_cast<unsigned>(units < 2 * 148 ? units : 2 * 148);
-        if (i8) grouped_small_kernel<true><<<grid, kSmallThreads, 0, stream>>>(m);
-        else grouped_small_kernel<false><<<grid, kSmallThreads, 0, stream>>>(m);
-        return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        const cudaError_t e = launch_chained(i8 ? grouped_small_kernel<true> : grouped_small_kernel<false>, dim3(grid),
+                                             kSmallThreads, 0, 1, stream, m);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     TcArgs a;
     memset(&a, 0, sizeof(a));

@@ -46,6 +46,34 @@ cudaError_t launch_swiglu(const RowsCall& c, cudaStream_t stream);
 cudaError_t launch_swiglu_grad(const RowsCall& c, cudaStream_t stream);
 cudaError_t launch_i8_rows(const RowsCall& c, cudaStream_t stream);
 
+// Programmatic dependent launch.  The operators are launched so that a kernel may
+// start while the one before it in the stream still runs: it sets itself up
+// (barriers, tensor memory, descriptors) and then waits, before its first access
+// to global memory, until that kernel has finished and its writes are visible.
+// Each lets its successor do the same from its own start on.
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                           cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster; attr[1].val.clusterDim.y = 1; attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // Reads and clears the current device's error word.
 moe_status_t grouped_status_read();
 

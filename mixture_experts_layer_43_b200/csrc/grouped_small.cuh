@@ -60,6 +60,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     bool bad = false;
+    grid_let_next();
+    grid_wait();
     for (int e0 = warp * 32; e0 < 1024; e0 += kSmallThreads) {
         const int i = e0 + lane;
         const int v = i < a.E ? a.offsets[i] : 0, next = i < a.E ? a.offsets[i + 1] : 0;

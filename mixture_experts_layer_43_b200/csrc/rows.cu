@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(const RowsCall c, c
     const int64_t n = c.rows * f.d;
     const uint16_t* gate = static_cast<const uint16_t*>(c.a);
     const uint16_t* up = static_cast<const uint16_t*>(c.b);
+    grid_let_next();
+    grid_wait();
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kRowThreads) + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
         int64_t r;
@@ -105,6 +107,8 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall
     const uint16_t* gate = static_cast<const uint16_t*>(c.a);
     const uint16_t* up = static_cast<const uint16_t*>(c.b);
     const uint16_t* dh = static_cast<const uint16_t*>(c.dh);
+    grid_let_next();
+    grid_wait();
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kRowThreads) + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
         int64_t r;
@@ -166,6 +170,8 @@ template <bool F16, bool GLU, int TPR, int VPT>
 __global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) {
     constexpr int kRows = kRowThreads / TPR;          // rows of a block
     __shared__ uint32_t s_max[kRowThreads / 32];
+    grid_let_next();
+    grid_wait();
     const int vec = c.cols / 8;
     const int t = threadIdx.x % TPR;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kRows) + threadIdx.x / TPR;
@@ -277,9 +283,10 @@ __global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) 
 }
 
 template <bool F16, bool GLU, int TPR, int VPT>
-void i8_rows_launch(const RowsCall& c, cudaStream_t stream) {
+cudaError_t i8_rows_launch(const RowsCall& c, cudaStream_t stream) {
     const int64_t blocks = (c.rows + kRowThreads / TPR - 1) / (kRowThreads / TPR);
-    i8_rows_kernel<F16, GLU, TPR, VPT><<<static_cast<unsigned>(blocks), kRowThreads, 0, stream>>>(c);
+    return launch_chained(i8_rows_kernel<F16, GLU, TPR, VPT>, dim3(static_cast<unsigned>(blocks)), kRowThreads, 0, 1,
+                          stream, c);
 }
 
 template <bool F16, bool GLU>
@@ -289,12 +296,11 @@ cudaError_t i8_rows(const RowsCall& c, cudaStream_t stream) {
     int tpr = 32;
     while (tpr < 256 && (c.cols > tpr * 32 || c.rows * tpr < 148 * kRowThreads)) tpr *= 2;
     switch (tpr) {
-        case 32: i8_rows_launch<F16, GLU, 32, 4>(c, stream); break;
-        case 64: i8_rows_launch<F16, GLU, 64, 4>(c, stream); break;
-        case 128: i8_rows_launch<F16, GLU, 128, 4>(c, stream); break;
-        default: i8_rows_launch<F16, GLU, 256, 4>(c, stream); break;
+        case 32: return i8_rows_launch<F16, GLU, 32, 4>(c, stream);
+        case 64: return i8_rows_launch<F16, GLU, 64, 4>(c, stream);
+        case 128: return i8_rows_launch<F16, GLU, 128, 4>(c, stream);
+        default: return i8_rows_launch<F16, GLU, 256, 4>(c, stream);
     }
-    return cudaGetLastError();
 }
 
 template <typename K>
@@ -302,8 +308,7 @@ cudaError_t flat(K small, K big, const RowsCall& c, cudaStream_t stream) {
     const int64_t n = c.rows * (c.cols / 8);
     const int64_t blocks = (n + kRowThreads - 1) / kRowThreads;
     const unsigned grid = static_cast<unsigned>(blocks < 148 * 64 ? blocks : 148 * 64);
-    (n < (int64_t(1) << 31) ? small : big)<<<grid, kRowThreads, 0, stream>>>(c, FastDiv(c.cols / 8));
-    return cudaGetLastError();
+    return launch_chained(n < (int64_t(1) << 31) ? small : big, dim3(grid), kRowThreads, 0, 1, stream, c, FastDiv(c.cols / 8));
 }
 
 }  // namespace
