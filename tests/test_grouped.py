@@ -679,6 +679,129 @@ def test_captured_calls_replay_with_new_offsets():
         assert all(torch.equal(a, b) for a, b in zip(replayed, outs))
 
 
+def _chain(st, between=lambda: None):
+    """Rounding, product, SwiGLU with rounding, product, gradient of SwiGLU, both gradients: every call reads what the
+    one before wrote.  `between` runs after each."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    counts, d, F = [70, 0, 9, 121], 256, 192
+    R, E = sum(counts), len(counts)
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    x = torch.randn((R, d), generator=gen, device="cuda").to(torch.bfloat16)
+    w8 = torch.randint(-127, 128, (E, 2 * F, d), generator=gen, device="cuda", dtype=torch.int32).to(torch.int8)
+    v8 = torch.randint(-127, 128, (E, d, F), generator=gen, device="cuda", dtype=torch.int32).to(torch.int8)
+    w = (w8.float() / 1000).to(torch.bfloat16)
+    ws, vs = torch.full((E, 2 * F), 1e-3, device="cuda"), torch.full((E, d), 1e-3, device="cuda")
+    q, s = torch.empty((R, d), dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    h, hs = torch.empty((R, F), dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    y = torch.empty((R, 2 * F), dtype=torch.bfloat16, device="cuda")
+    z, dx = torch.empty_like(x), torch.empty_like(x)
+    dw = torch.empty(w.shape, device="cuda")
+    up = B.moe_grouped_t(R, E, d, 2 * F, 3, 0, 0, off.data_ptr(), d, 2 * F)
+    dn = B.moe_grouped_t(R, E, F, d, 3, 0, 0, off.data_ptr(), F, d)
+    up16 = B.moe_grouped_t(R, E, d, 2 * F, 0, 0, 0, off.data_ptr(), d, 2 * F)
+    up32 = B.moe_grouped_t(R, E, d, 2 * F, 0, 2, 0, off.data_ptr(), d, 2 * F)
+    torch.cuda.synchronize()
+    calls = [
+        lambda: B.moe_i8_quantize(R, d, 0, x.data_ptr(), d, q.data_ptr(), d, s.data_ptr(), st),
+        lambda: B.moe_i8_grouped_gemm(up, q.data_ptr(), s.data_ptr(), w8.data_ptr(), ws.data_ptr(), y.data_ptr(), st),
+        lambda: B.moe_swiglu_i8(R, F, 0, y.data_ptr(), y.data_ptr() + 2 * F, 2 * F, h.data_ptr(), F, hs.data_ptr(), st),
+        lambda: B.moe_i8_grouped_gemm(dn, h.data_ptr(), hs.data_ptr(), v8.data_ptr(), vs.data_ptr(), z.data_ptr(), st),
+        lambda: B.moe_swiglu_grad(R, F, 0, z.data_ptr(), d, y.data_ptr(), y.data_ptr() + 2 * F, 2 * F, y.data_ptr(),
+                                  y.data_ptr() + 2 * F, 2 * F, st),
+        lambda: B.moe_grouped_dgrad(up16, y.data_ptr(), w.data_ptr(), dx.data_ptr(), st),
+        lambda: B.moe_grouped_wgrad(up32, y.data_ptr(), x.data_ptr(), dw.data_ptr(), st),
+        lambda: B.moe_swiglu(R, F, 0, dx.data_ptr(), dx.data_ptr() + 128, d, x.data_ptr(), d, st),
+    ]
+
+    def step():
+        for c in calls:
+            c()
+            between()
+
+    step.offsets = off                             # the descriptions hold its address alone
+    return step, (x, q, s, h, hs, y, z, dx, dw)
+
+
+def test_a_chain_of_calls_needs_no_synchronisation():
+    """Kernels of the chain start while their predecessors still run: five rounds without a wait between any two calls
+    give what rounds with one after every call give; the last call overwrites what the first of the next round reads."""
+    step, outs = _chain(_stream(), torch.cuda.synchronize)
+    for _ in range(5):
+        step()
+    _ok()
+    want = [o.clone() for o in outs]
+    for _ in range(6):
+        step, outs = _chain(_stream())
+        for _ in range(5):
+            step()
+        _ok()
+        for a, b in zip(outs, want):
+            assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+
+
+def test_two_captured_graphs_at_once():
+    """Two graphs of the chain, each with its own tensors, replayed side by side on two streams."""
+    graphs, outs = [], []
+    for _ in range(2):
+        _chain(_stream())[0]()                      # a first call outside the capture
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            step, o = _chain(s.cuda_stream)
+            start = [v.clone() for v in o]
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                step()
+        graphs.append((graph, s, start, step))
+        outs.append(o)
+    torch.cuda.synchronize()
+    for (_graph, _s, start, _step), o in zip(graphs, outs):
+        for v, to in zip(start, o):
+            to.copy_(v)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, s, _start, _step in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    _ok()
+    step, want = _chain(_stream())
+    for _ in range(3):
+        step()
+    _ok()
+    for o in outs:
+        for a, b in zip(o, want):
+            assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+
+
+@pytest.mark.parametrize("counts", [[30, 2, 70], [1, 1]], ids=str)
+def test_pointers_on_any_16_byte_boundary(counts):
+    """Every tensor 16 bytes past a 256-byte boundary."""
+    G = Group(counts, 72, 136, "bf16")
+
+    def off16(t):
+        buf = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")
+        v = buf[16:].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        return v
+
+    x, w, dy = off16(G.rows_in("x", 1.0)), off16(G.weights()), off16(G.rows_in("y", 1.0))
+    y, dx, dw = off16(G.rows_out("y", "bf16")), off16(G.rows_out("x", "bf16")), off16(torch.zeros_like(w))
+    assert x.data_ptr() % 256 == 16
+    B.moe_grouped_gemm(G.g("bf16"), x.data_ptr(), w.data_ptr(), y.data_ptr(), _stream())
+    B.moe_grouped_dgrad(G.g("bf16"), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), _stream())
+    B.moe_grouped_wgrad(G.g("bf16"), dy.data_ptr(), x.data_ptr(), dw.data_ptr(), _stream())
+    _ok()
+    a, b, c = torch.empty_like(y), torch.empty_like(dx), torch.empty_like(dw)
+    x, w, dy = x.clone(), w.clone(), dy.clone()
+    B.moe_grouped_gemm(G.g("bf16"), x.data_ptr(), w.data_ptr(), a.data_ptr(), _stream())
+    B.moe_grouped_dgrad(G.g("bf16"), dy.data_ptr(), w.data_ptr(), b.data_ptr(), _stream())
+    B.moe_grouped_wgrad(G.g("bf16"), dy.data_ptr(), x.data_ptr(), c.data_ptr(), _stream())
+    _ok()
+    assert torch.equal(a, y) and torch.equal(b, dx) and torch.equal(c, dw)
+
+
 @pytest.mark.parametrize("acc", [0, 1])
 def test_the_same_call_gives_the_same_bits(acc):
     G = Group([700, 3, 0, 260], 264, 520, "bf16")
