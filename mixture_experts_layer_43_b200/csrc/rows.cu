@@ -39,18 +39,17 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret
 // sigmoid(g) = 1 / (1 + 2^t), t = -g log2(e).  t is formed in two parts, since
 // the rounding of t alone would cost |g| half steps of the result: 2^t =
 // 2^hi (1 + lo ln 2).  Errors in units of 2^-24: 2^hi 4 (ex2.approx), 1 + lo
-// ln 2 and the product 1 each, 1 + 2^t 1, the reciprocal 2: at most 9.  For g <
-// -88.7 the power is infinite and the result 0, as with any fp32 exponential;
-// lo is dropped where t is so large (it would be NaN at an infinity).
+// ln 2 and the product 1 each, 1 + 2^t 1, the reciprocal 2: at most 9.  Below
+// g = -87.3 the result is under 2^-126 and taken as 0.  At an infinity lo is NaN:
+// fminf drops it (the factor is never above 1.0001 otherwise).
 __device__ __forceinline__ float sigmoid_f(float g) {
     constexpr float kL = -1.44269504f, kLlo = -1.92596299e-8f, kLn2 = 0.693147181f;
     const float hi = g * kL;
-    float lo = fmaf(g, kLlo, fmaf(g, kL, -hi));
-    lo = fabsf(hi) < 256.f ? lo : 0.f;
+    const float lo = fmaf(g, kLlo, fmaf(g, kL, -hi));
     float p, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(hi));
-    p *= fmaf(lo, kLn2, 1.f);
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(hi));
+    p *= fminf(fmaf(lo, kLn2, 1.f), 1.0001f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
     return r;
 }
 
@@ -135,12 +134,12 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall
 
 // Codes of 8 values v: q = rint(v / s), the quotient rounded to nearest first.
 // v * (1 / s) is within 127 * 3 * 2^-24 < 2.3e-5 of that quotient (the sum and
-// the difference below are rounded once each), so it rounds
-// to the same integer unless it lies within 3e-5 of a half; only then is the
-// division done.  Adding 1.5 * 2^23 rounds to the nearest
-// integer, ties to even, and leaves it in the low byte.
+// the difference below are rounded once each), so it rounds to the same integer
+// unless it lies within 3e-5 of a half; only for such a value is the division
+// done.  Adding 1.5 * 2^23 rounds to the nearest integer, ties to even, and
+// leaves it in the low byte.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float inv) {
-    constexpr float kMagic = 12582912.f;
+    constexpr float kMagic = 12582912.f, kNear = 0.49997f;
     uint32_t b[8];
     float off = 0.f;
 #pragma unroll
@@ -149,9 +148,11 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float inv)
         off = fmaxf(off, fabsf(fmaf(v[i], inv, kMagic - t)));
         b[i] = __float_as_uint(t);
     }
-    if (off > 0.49997f) {
+    if (off > kNear) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], s)))));
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(fmaf(v[i], inv, kMagic - __uint_as_float(b[i]))) > kNear)
+                b[i] = __float_as_uint(__fdiv_rn(v[i], s) + kMagic);
     }
     return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
                       __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
@@ -167,7 +168,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float inv)
 // between the two passes (as they were loaded; SwiGLU's as computed); what a
 // longer row has beyond that is read again.
 template <bool F16, bool GLU, int TPR, int VPT>
-__global__ void __launch_bounds__(kRowThreads) i8_rows_kernel(const RowsCall c) {
+__global__ void __launch_bounds__(kRowThreads, GLU ? 4 : 5) i8_rows_kernel(const RowsCall c) {
     constexpr int kRows = kRowThreads / TPR;          // rows of a block
     __shared__ uint32_t s_max[kRowThreads / 32];
     grid_let_next();

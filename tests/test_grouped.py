@@ -52,6 +52,10 @@ def _ok():
 
 def _within(got, ref, tol, what):
     d = (got.double() - ref).abs()
+    # a value half a step or more above the largest number of its type rounds to infinity
+    info = torch.finfo(got.dtype)
+    over = got.isinf() & (ref.abs() >= info.max * (1 + info.eps / 4)) & (torch.sign(got).double() == torch.sign(ref))
+    d = torch.where(over, 0.0, d)
     worst = (d - tol).max().item() if d.numel() else 0.0
     assert d.numel() == 0 or bool((d <= tol).all()), \
         f"{what}: {int((~(d <= tol)).sum())} of {d.numel()} outside, worst by {worst:.3g}"
@@ -360,6 +364,7 @@ def test_swiglu_and_its_gradient(rows, cols, dtype):
     gen.manual_seed(rows + cols)
     gu = (torch.randn((rows, 2 * cols + 16), generator=gen, device="cuda") * 4).to(T[dtype])
     gu[0, :4] = torch.tensor([-100.0, 100.0, 0.0, -1.28], device="cuda").to(T[dtype])
+    gu[0, 4:8] = torch.tensor([-60.0, 60.0, -20.0, 1e4], device="cuda").to(T[dtype])
     gate, up = gu[:, :cols], gu[:, cols:2 * cols]
     dh = torch.randn((rows, cols + 8), generator=gen, device="cuda").to(T[dtype])
     h = torch.full((rows, cols + 8), -77.0, device="cuda").to(T[dtype])
@@ -391,6 +396,22 @@ def test_swiglu_and_its_gradient(rows, cols, dtype):
     B.moe_swiglu(rows, cols, MOE[dtype], over.data_ptr(), over.data_ptr() + 2 * cols, st,
                  over.data_ptr() + 2 * cols, st, _stream())
     assert torch.equal(over[:, cols:2 * cols], h[:, :cols])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_swiglu_of_infinities_and_nan(dtype):
+    """As the formula in fp32 has it: silu(inf) = inf, silu(-inf) = -inf * 0 = NaN, NaN stays NaN; the neighbours of
+    such values are not touched."""
+    inf, nan = float("inf"), float("nan")
+    g = torch.tensor([inf, -inf, nan, 1.0, 0.0, 2.0, inf, -3.0], device="cuda").to(T[dtype])[None].contiguous()
+    u = torch.tensor([2.0, 2.0, 2.0, inf, inf, nan, -1.0, 0.5], device="cuda").to(T[dtype])[None].contiguous()
+    h = torch.empty_like(g)
+    B.moe_swiglu(1, 8, MOE[dtype], g.data_ptr(), u.data_ptr(), 8, h.data_ptr(), 8, _stream())
+    want = g.float() / (1 + torch.exp(-g.float())) * u.float()
+    assert torch.equal(h.isnan(), want.isnan()) and torch.equal(h.isinf(), want.isinf())
+    assert torch.equal(torch.sign(h[h.isinf()]), torch.sign(want[want.isinf()]).to(T[dtype]))
+    ref = _swiglu64(g, u)[0, 7]
+    _within(h[0, 7:], ref[None], _rounding(ref[None], dtype) + ref.abs() * (11 * U24), "h")
 
 
 def test_swiglu_gradient_against_differences():
@@ -453,6 +474,27 @@ def test_i8_rows(rows, cols, dtype):
     _check_codes(q[normal, :cols], scale[:rows][normal], v64[normal], 11 * U24)
     if rows > 2:
         assert scale[1].item() == 0.0 and bool((q[1, :cols] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_i8_ties_go_to_even(dtype):
+    """Quotients that lie exactly on a half, for scales of 1, of a large and of a tiny power of two, and quotients next
+    to a half (a scale of 1/127 of a power of two: v 127 / 2^k rounds to either side)."""
+    half = torch.arange(128, device="cuda", dtype=torch.float32) - 63.5          # exact in bf16 too
+    for k in ([0, 8, -9] if dtype == "f16" else [0, 60, -60]):
+        x = torch.cat([half, torch.tensor([127.0], device="cuda").expand(8)]) * 2.0 ** k
+        x = x.to(T[dtype]).repeat(3, 1)
+        q, s = torch.empty((3, 136), dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+        B.moe_i8_quantize(3, 136, MOE[dtype], x.data_ptr(), 136, q.data_ptr(), 136, s.data_ptr(), _stream())
+        assert bool((s == 2.0 ** k).all())
+        assert torch.equal(q[1].float(), torch.round(x[1].float() / 2.0 ** k))
+    v = torch.arange(1, 1025, device="cuda", dtype=torch.float32).to(T[dtype]).view(8, 128)
+    v[:, 0] = 1024.0
+    q, s = torch.empty((8, 128), dtype=torch.int8, device="cuda"), torch.empty(8, device="cuda")
+    B.moe_i8_quantize(8, 128, MOE[dtype], v.data_ptr(), 128, q.data_ptr(), 128, s.data_ptr(), _stream())
+    host = v.float().cpu().numpy()
+    scale = np.abs(host).max(1) / np.float32(127)
+    assert np.array_equal(q.cpu().numpy(), np.rint(host / scale[:, None]).astype(np.int8))
 
 
 @pytest.mark.parametrize("cols", [64, 4096, 16384])
