@@ -539,6 +539,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             uint32_t phase = 0;
             uint32_t pad_phase = 0;                  // a bit for each stage: uses of its padded[]
             while (walk.next(g)) {
+                if (OP == kOpWgrad && g.nk == 0) continue;     // no rows: the epilogue stores zeros by itself
                 const uint32_t idesc = a.idesc | (static_cast<uint32_t>(g.cols >> 3) << 17);
                 // full steps, then (wgrad) a last one of 1 to 4 slices of 16 rows
                 const int n_full = OP == kOpWgrad && (g.valid & 63) ? g.nk - 1 : g.nk;
@@ -600,7 +601,18 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             const int valid = OP == kOpWgrad ? min(kTile, a.N - g.n0) : g.valid;
             const int64_t col0 = OP == kOpWgrad ? static_cast<int64_t>(g.e) * a.N + g.n0 : g.row0;
             const bool empty_expert = OP == kOpWgrad && g.nk == 0;
-            bool store = f0 < a.M && !(empty_expert && a.accumulate);
+            bool store = f0 < a.M;
+            if (empty_expert) {                               // zeros by 16 bytes, or nothing to add
+                store = false;
+                const int es = a.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+                const int f_cta = g.m0 + kHalf * rank;
+                const int units = min(kHalf, a.M - f_cta) * es / 16;      // of a row of this CTA's
+                uint8_t* o = static_cast<uint8_t*>(a.out) + (col0 * a.out_stride + f_cta) * es;
+                if (units > 0 && pair == 0 && !a.accumulate)
+                    for (int i = (warp - 2) * 32 + lane; i < valid * units; i += kEpiWarps * 32)
+                        *reinterpret_cast<uint4*>(o + (i / units) * a.out_stride * es + (i % units) * 16) =
+                            make_uint4(0, 0, 0, 0);
+            }
             auto scale_of = [&](int c) {                      // 8 bits: of this lane's token of column c ..
                 return I8 && c + lane < valid ? a.a_scale[col0 + c + lane] : 0.f;
             };
@@ -614,7 +626,8 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
                 const bool none = g.k_from == g.k_to;
-                const int segments = F32 && !none ? (g.k_to - g.k_from + kSegment - 1) / kSegment : 1;
+                const int segments =
+                    empty_expert ? 0 : F32 && !none ? (g.k_to - g.k_from + kSegment - 1) / kSegment : 1;
                 for (int seg = 0; seg < segments; ++seg, ++local) {
                     const int b = local & 1;
                     // every decision before the warp-collective tcgen05.ld is warp-uniform
@@ -703,13 +716,14 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                 // tiles of few rows pass through both
                 const int part = first_part ^ b;
                 float as = scale_of(part * 32);
-                const bool ok = !__any_sync(0xffffffffu, !wait(tfull_u + b * 8, (local >> 1) & 1));
-                ++local;
-                if (!ok) continue;
-                tc_fence_after();
+                if (!empty_expert) {
+                    ++local;
+                    if (__any_sync(0xffffffffu, !wait(tfull_u + b * 8, ((local - 1) >> 1) & 1))) continue;
+                    tc_fence_after();
+                }
                 const uint32_t taddr = lanes + b * kTile;
                 uint32_t v[2][32];
-                if (store && part * 32 < valid && !empty_expert) tmem_ld32(taddr + part * 32, v[0]);
+                if (store && part * 32 < valid) tmem_ld32(taddr + part * 32, v[0]);
 #pragma unroll 1
                 for (int c0 = part * 32; store && c0 < valid; c0 += 128) {
 #pragma unroll
@@ -717,19 +731,17 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                         const int c = c0 + j * 64;
                         if (c >= valid) break;
                         tmem_ld_wait();
-                        if (c + 64 < valid && !empty_expert) tmem_ld32(taddr + c + 64, v[j ^ 1]);
+                        if (c + 64 < valid) tmem_ld32(taddr + c + 64, v[j ^ 1]);
                         const float next_as = scale_of(c + 64);
-                        if (empty_expert) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[j][i] = 0u;
-                        }
                         store_columns<I8>(a, v[j], col0 + c, valid - c, f, f0, ws, as, own);
                         as = next_as;
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, leader));
+                if (!empty_expert) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_u + b * 8, leader));
+                }
             }
         }
     } else {

@@ -186,6 +186,7 @@ CASES = [
     ([1500], 128, 384, {}),
     ([5] * 300, 96, 72, {}),
     ([2] * 512 + [0] * 511 + [9], 64, 40, {}),
+    (([0] * 7 + [50] + [0, 3]) * 20, 328, 264, dict(behind=3)),
 ]
 
 
