@@ -407,11 +407,14 @@ moe_status_t moe_bf16_to_f16(const void* src, int64_t n, void* dst, void* stream
  * products grouped by expert with their two gradients, SwiGLU rows with their
  * gradient, and the same path with 8-bit activations and weights.  The pages
  * have no counterpart (they describe inference through the fused layer only).
- * They need no plan and keep no state between calls, so calls may run side by
- * side on several streams; each runs on the current device, where all of its
- * pointers must live (INVALID_ARG otherwise).  A first call on a device may
- * load the library's module and raises the kernels' shared-memory limits:
- * make it before a stream capture.  Outputs must not overlap inputs, except
+ * They need no plan and keep no state between calls, so their work may run side
+ * by side on several streams (issue the calls from one host thread at a time, as
+ * everywhere in this library); each runs on the current device, where all of its
+ * pointers must live (INVALID_ARG otherwise).  A first call on a device may load
+ * the library's module and raises the kernels' shared-memory limits: make it
+ * before a stream capture.  In a stream a call may start its set-up while the
+ * one before it still runs (programmatic dependent launch); it touches memory
+ * only after that one has finished.  Outputs must not overlap inputs, except
  * where it says so. */
 typedef enum moe_dtype {
     MOE_DTYPE_BF16 = 0,
@@ -441,8 +444,9 @@ typedef struct moe_grouped {
 } moe_grouped_t;
 
 /* y[r] = W[e] x[r] for the rows r of each expert e: x [rows][d_in],
- * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once.  Every
- * row's result depends on its own x and its expert's weights alone. */
+ * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once (an F32
+ * result is within about 1e-6 of the sum).  Every row's result depends on its
+ * own x and its expert's weights alone. */
 moe_status_t moe_grouped_gemm(const moe_grouped_t* g, const void* x, const void* w, void* y,
                               void* stream);
 
@@ -452,7 +456,8 @@ moe_status_t moe_grouped_dgrad(const moe_grouped_t* g, const void* dy, const voi
 
 /* The gradient of its weights: dw[e] = sum over e's rows of dy[r] x[r]^T,
  * dw [E][d_out][d_in] of out_dtype.  An expert without rows gets zeros (with
- * accumulate: is left as it was).  The order of the sums is fixed. */
+ * accumulate: is left as it was).  The order of the sums is fixed.  The addition
+ * of accumulate takes subnormal numbers as zero. */
 moe_status_t moe_grouped_wgrad(const moe_grouped_t* g, const void* dy, const void* x, void* dw,
                                void* stream);
 

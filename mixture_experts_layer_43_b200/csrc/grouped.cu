@@ -21,9 +21,21 @@
 // since they hold another expert's values (and 0 * NaN would not vanish).
 //
 // Roles of a CTA: warp 0 loads by TMA into a ring of six 32 KB stages, warp 1
-// of the pair's first CTA issues the MMAs, four warps drain the accumulator
-// (two of 256 TMEM columns each, so that they overlap the next tile's MMAs);
-// wgrad has one more warp that zeroes the rows of the last step.
+// of the pair's first CTA issues the MMAs, eight warps drain the accumulator
+// (two of 256 TMEM columns each, so that they overlap the next tile's MMAs) and
+// store it, lanes along the contiguous dimension; wgrad has one more warp that
+// zeroes the rows of the last step.
+//
+// What bounds it.  A stage costs 512 cycles of MMA at 256 columns and takes 32 KB
+// into each SM's shared memory, near what an SM can fill (64 B a cycle), so loads
+// and MMAs have to overlap without a gap: both warps run their loops converged,
+// with one elected lane issuing (a loop run by a single lane took 250 cycles for
+// an MMA of any width, the descriptors' moves between register files standing in
+// its way; now 138 K cycles for 131 K of MMA in a product of one expert).  On a
+// DeepSeek-shaped prompt (24576 rows, 64 experts of 2048 x 2816, Zipf loads) the
+// tensor pipe is active in 65% of the cycles and DRAM moves the algorithm's bytes
+// once (977 MB); over half a second of such calls the power cap, not the kernel,
+// sets the time (244 us in a short run, 285 us sustained).
 #include <atomic>
 
 #include <cudaTypedefs.h>
@@ -172,8 +184,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     return mbar_try_wait_cluster(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
 }
 
-// A tile of the product.  gemm and dgrad: feature rows m0.., token rows
-// row0 .. row0 + valid - 1 as columns.  wgrad: weight rows m0.., columns n0..,
+// A tile of the product.  gemm and dgrad: features m0.., token rows row0 .. row0 +
+// valid - 1 as columns.  wgrad: elements m0.. of the rows n0.. of dW[e], the
 // reduction over row0 .. row0 + valid - 1.
 struct Tile {
     int e, m0, n0, row0, valid;
@@ -192,7 +204,7 @@ struct TileWalk {
     const int* off;        // in shared memory (wgrad: the caller's table)
     const int* base;       // gemm, dgrad: row chunks of the experts before e
     int mt, nt;
-    int t, total;          // fits: the launch checks it
+    int t, total;          // both, and t + step, fit: the launch checks it
     int step, pair, e = 0;
 
     __device__ TileWalk(const TcArgs& args, const int* s_off, const int* s_base, int first, int n, int of_tile)
@@ -810,9 +822,7 @@ bool tile_map(CUtensorMap* m, int elem, const void* base, int nd, const uint64_t
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
     if (!enc) return false;
     const cuuint32_t es[3] = {1, 1, 1};
-    const CUtensorMapDataType t = elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                : elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType t = elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return enc(m, t, nd, const_cast<void*>(base), dims, pitch, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1005,9 +1015,8 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         tiles = static_cast<int64_t>(c.E) * ceil_div(a.M, kTile) * ceil_div(a.N, kTile);
         nk = static_cast<int>(ceil_div(c.rows, 64 * static_cast<int64_t>(c.E)));            // on average
         cols = a.N < kTile ? a.N : kTile;
-
     }
-    if (!ok || tiles > 0x7FFFFFFF) return MOE_ERR_INVALID_ARG;
+    if (!ok || tiles > 0x7FFF0000) return MOE_ERR_INVALID_ARG;
     if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, nk, cols, stream);
     if (c.out_dtype == MOE_DTYPE_F32) {
         if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, nk, cols, stream);

@@ -70,7 +70,9 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
     attr[1].val.clusterDim.x = cluster; attr[1].val.clusterDim.y = 1; attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();          // reported by the caller's status alone
+    return e;
 }
 #endif
 

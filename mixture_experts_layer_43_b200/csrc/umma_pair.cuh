@@ -1,6 +1,6 @@
-// umma_pair.cuh -- primitives of a CTA pair (a cluster of two CTAs that runs
-// tcgen05.mma.cta_group::2), shared by the prefill GEMMs and the grouped
-// products.
+// umma_pair.cuh -- primitives of a CTA pair (two CTAs of a cluster that run
+// tcgen05.mma.cta_group::2) for the grouped products.  prefill.cu keeps its own:
+// the committed counters of its kernels name the hash of its source.
 #pragma once
 
 #include "moe_internal.cuh"
@@ -26,16 +26,6 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
 }
-// TMA tile load into this CTA's shared memory whose transaction bytes
-// complete on the mbarrier at `mbar` (shared::cluster address: the pair's
-// first CTA).  No multicast.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t mbar,
-                                                 int32_t c0, int32_t c1, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;"
-        :: "r"(smem_u32(dst)), "l"(map), "r"(mbar), "r"(c0), "r"(c1), "l"(policy) : "memory");
-}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
@@ -52,13 +42,6 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
         " setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-// Arrive on `bar` (same offset) in both CTAs of the pair once every MMA this
-// thread issued so far completes.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
 }  // namespace moe
