@@ -449,11 +449,12 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
         if (OP != kOpWgrad) prefetch_tensormap(&a.tmB128);
     }
     grid_let_next();
-    grid_wait();
-    const bool sound = load_offsets<OP>(a, s_off, s_base, s_warp);   // the same in both CTAs
     tc_fence_before();
     cluster_sync_all();       // the peer's barriers are initialised before any signal
     tc_fence_after();
+    grid_wait();
+    const bool sound = load_offsets<OP>(a, s_off, s_base, s_warp);   // the same in every CTA
+    __syncthreads();
     if (!sound) {
         if (tid == 0) atomicOr(&g_grouped_err, kErrBadId);
         if (warp == 1) tmem_dealloc_pair(*s_tmem, 512);

@@ -818,6 +818,47 @@ def test_two_captured_graphs_at_once():
             assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
 
 
+def test_captured_behind_copies_and_joined_streams():
+    """A call captured behind a memset, a device copy, and two branches that another stream runs: it still waits for
+    all of them."""
+    G = Group([40, 10, 14], 128, 256, "bf16")
+    src = [G.rows_in("x", 1.0) for _ in range(3)]
+    x, w, y, z = G.rows_in("x", 1.0), G.weights(), G.rows_out("y", "bf16"), G.rows_out("y", "bf16")
+    big = torch.randn((4096, 4096), device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def gemm(a, out):
+        B.moe_grouped_gemm(G.g("bf16"), a.data_ptr(), w.data_ptr(), out.data_ptr(), _stream())
+
+    gemm(x, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        y.zero_()
+        x.copy_(src[0])
+        gemm(x, y)                                  # behind a copy
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            slow = big.sin().cos().exp().sin()      # the branch that takes longer
+            src[2].copy_(torch.where(slow.sum() > float("inf"), src[0], src[1]))
+        x.copy_(src[0] + src[0])
+        main.wait_stream(side)
+        gemm(src[2], z)                             # behind both branches
+        gemm(x, y)                                  # behind a kernel of its own kind
+    for _ in range(3):
+        src[0].normal_()
+        src[1].normal_()
+        src[2].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got_y, got_z = y.clone(), z.clone()
+        gemm(src[1], z)
+        torch.cuda.synchronize()
+        gemm(src[0] + src[0], y)
+        _ok()
+        assert torch.equal(got_z, z) and torch.equal(got_y, y)
+
+
 @pytest.mark.parametrize("counts", [[30, 2, 70], [1, 1]], ids=str)
 def test_pointers_on_any_16_byte_boundary(counts):
     """Every tensor 16 bytes past a 256-byte boundary."""
