@@ -222,8 +222,9 @@ struct TileWalk {
             // the shorter side varies fastest: its operand is what L2 keeps
             g.m0 = (mt < nt ? r % mt : r / nt) * kTile;
             g.n0 = (mt < nt ? r / mt : r % nt) * kTile;
-            g.row0 = off[g.e];
-            g.valid = off[g.e + 1] - g.row0;
+            // read again by every role: clamped, should the table change under the call
+            g.row0 = max(0, off[g.e]);
+            g.valid = max(0, static_cast<int>(min(static_cast<int64_t>(off[g.e + 1]), a.rows)) - g.row0);
             g.cols = (min(kTile, a.N - g.n0) + 31) & ~31;
             g.nk = (g.valid + 63) / 64;
         } else {

@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
         const uint32_t m = __shfl_sync(0xffffffffu, has, word);
         n.e = word * 32 + __fns(m, 0, want - __shfl_sync(0xffffffffu, before, word) + 1);
         n.f0 = static_cast<int>(unit - static_cast<int64_t>(want) * tiles) * kSmallRows;
-        n.tok = a.offsets[n.e];
-        n.hi = a.offsets[n.e + 1];
+        // read again: clamped, should the table change under the call
+        n.tok = max(0, a.offsets[n.e]);
+        n.hi = static_cast<int>(min(static_cast<int64_t>(a.offsets[n.e + 1]), a.rows));
     };
     auto advance = [&](SmallUnit& n) {                 // the next rows, or the next unit
         if (n.tok + kSmallTok < n.hi) {
