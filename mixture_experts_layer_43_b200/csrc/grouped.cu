@@ -919,16 +919,23 @@ moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t 
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Whether a product goes to grouped_small_kernel: its 256-row weight tiles keep
-// at most half of the CTA pairs busy, and its experts average at most 16 rows
-// (a second pass over weights that L1 and L2 hold).  Measured, small / tensor
-// cores: 8 experts of 2048 x 1024, a row each (32 tiles) 9.9 / 13.8 us; one of
-// 4096 x 4096 (16 tiles) with 1 row 7.9 / 19.0 us, with 32 rows 24.9 / 19.1 us; 16
-// experts of 2048 x 1024 (64 tiles) 18.8 / 16.6 us, 8 of 512 x 2048 (64 tiles) 10.1
-// / 8.2 us, 2 of 4096 x 28672 (224 tiles) 99 / 91 us.
+// Whether a product goes to grouped_small_kernel.  Measured, small / tensor cores:
+//  - its 256-row weight tiles keep at most half of the CTA pairs busy, and its
+//    experts average at most 16 rows (a second pass over weights that L1 and L2
+//    hold): 8 experts of 2048 x 1024, a row each (32 tiles) 9.6 / 11.5 us; one of 4096
+//    x 4096 (16 tiles) with 1 row 8.0 / 13.1 us, with 16 rows 12.5 / 13.4; but 16
+//    experts of 2048 x 1024 (64 tiles) 18.6 / 14.9, 8 of 512 x 2048 (64) 9.2 / 7.2;
+//  - or its tiles are long (8192 weights a row) and make one to two waves, the
+//    second of which would leave pairs idle, and its experts average at most 2
+//    rows: 8 experts of 14336 x 4096 (128 tiles at most) with 8 rows 122 / 135 us, with
+//    16 rows 135 / 142, of 8192 x 4096 82 / 87, in 8 bits 77 / 82; but with 32 rows 181 /
+//    149, and 48 experts of 8192 x 1024 (192 tiles) 101 / 95, 8 of 4096 x 28672 (896
+//    tiles) 277 / 241.
 bool few_rows(const GroupedCall& c) {
     const int64_t slots = c.rows < c.E ? c.rows : c.E;      // experts with rows, at most
-    return slots * ceil_div(c.d_out, kTile) <= 37 && c.rows <= 16 * slots;
+    const int64_t tiles = slots * ceil_div(c.d_out, kTile);
+    if (tiles <= 37) return c.rows <= 16 * slots;
+    return tiles > 74 && tiles <= 148 && c.rows <= 2 * slots && c.d_in >= 8192;
 }
 
 }  // namespace

@@ -218,6 +218,7 @@ LONG = [
     ([1, 300], 1544, 8, {}),
     ([17], 2048, 3336, {}),
     ([3], 4104, 24, {}),
+    ([2, 0, 9, 1, 0, 4, 0, 0], 8200, 4104, dict(before=1, pad_x=8)),
 ]
 
 
@@ -225,7 +226,8 @@ LONG = [
 @pytest.mark.parametrize("counts,d_in,d_out,kw", LONG, ids=lambda v: str(v)[:24])
 def test_long_reductions_over_few_tiles(counts, d_in, d_out, kw, dtype, out):
     check_gemm(Group(counts, d_in, d_out, dtype, **kw), out)
-    check_dgrad(Group(counts, d_out, d_in, dtype, **kw), out)
+    swapped = {**kw, "pad_x": kw.get("pad_y", 0), "pad_y": kw.get("pad_x", 0)}
+    check_dgrad(Group(counts, d_out, d_in, dtype, **swapped), out)
 
 
 @pytest.mark.parametrize("dtype,out,acc", [("bf16", "bf16", False), ("f16", "f32", False), ("bf16", "f32", True)])
