@@ -53,6 +53,12 @@ __device__ __forceinline__ void small_mma(uint32_t (&c)[4], uint32_t a0, uint32_
     }
 }
 
+// 16 bytes by an ordinary load.  x and the weights may be what the kernel before
+// this one wrote while this one was already resident (programmatic dependent
+// launch), so they are not read-only for as long as this kernel lives and the
+// non-coherent path (__ldg, ld.global.nc) is not open to them.
+__device__ __forceinline__ uint4 small_load(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
 // The piece of work a block is at: 16 output features of an expert and up to 8
 // of its rows.
 struct SmallUnit {
@@ -120,8 +126,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
         for (int u = 0; u < 4; ++u) {
             const int k = k0 + u * 64 + t * 16;
             const bool in = k < a.k_bytes;
-            al[u] = in && ok_lo ? __ldg(reinterpret_cast<const uint4*>(w + k)) : zero;
-            ah[u] = in && ok_hi ? __ldg(reinterpret_cast<const uint4*>(w + 8 * static_cast<int64_t>(a.k_bytes) + k)) : zero;
+            al[u] = in && ok_lo ? small_load(w + k) : zero;
+            ah[u] = in && ok_hi ? small_load(w + 8 * static_cast<int64_t>(a.k_bytes) + k) : zero;
         }
     };
     SmallUnit cur, next;
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
                 const int k = k0 + u * 64 + t * 16;
                 cl[u] = al[u];
                 ch[u] = ah[u];
-                cb[u] = k < a.k_bytes && ok_x ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+                cb[u] = k < a.k_bytes && ok_x ? small_load(x + k) : zero;
             }
             k0 += kSmallWarps * kSmallStep;
             if (k0 < a.k_bytes) fetch(cur, k0);
