@@ -50,8 +50,6 @@ static __device__ uint32_t g_grouped_err;
 
 namespace {
 
-#include "grouped_small.cuh"
-
 constexpr int kMaxDevices = 64;
 constexpr int kTile = 256;                        // tile rows (M), and the most columns (N)
 constexpr int kHalf = 128;                        // rows of the tile one CTA holds
@@ -65,6 +63,9 @@ constexpr int kStages = 6;
 // roundings to nearest (measured over 1024 rows: 1.0e-6 of the result in one
 // sum).  A 16-bit result does not show it.
 constexpr int kSegment = 8;
+
+#include "grouped_small.cuh"
+
 constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
 constexpr int kEpiWarps = 8;                      // two for each quarter of the TMEM lanes
 constexpr int kEpiBytes = kEpiWarps * 128;        // 8 bits: 32 scales for each

@@ -11,7 +11,11 @@
 // fragment's slots stand for does not matter as long as both sides agree, so a
 // lane's 16 consecutive bytes feed two MMAs as they are, and nothing passes
 // through shared memory but the eight warps' partial sums (added in order; two
-// sets of them, so that a piece costs one barrier).
+// sets of them, so that a piece costs one barrier).  Over a long reduction a warp
+// adds its accumulators to its partial sum, in fp32 rounded to nearest, after each
+// kSegment steps and starts them anew: like a tile's accumulator, they lose up to
+// a unit of fp32 with every MMA, always towards zero (65536 terms in one sum: 1.1e-5
+// of the result in bf16, 2.4e-5 in fp16).
 //
 // Two blocks an SM keep 128 KB of weights in flight: 16 rows through 8 experts of
 // 14336 x 4096 (fp16) take 135 us, 6.1 TB/s; one row through 4096 x 4096 8.0 us, of
@@ -143,6 +147,22 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
         const bool ok_x = cur.tok + g < cur.hi;
         uint32_t c[4] = {0, 0, 0, 0}, d[4] = {0, 0, 0, 0};    // two sums: half as many cuts to fp32 in each
         int k0 = k_first;
+        bool begun = false;                            // the partial sum holds something
+        auto fold = [&] {                              // every thread its own four words
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t& p = part[warp][2 * t + (i & 1)][g + 8 * (i >> 1)];
+                if constexpr (I8) {
+                    p = c[i] + d[i];
+                } else {
+                    const float sum = __uint_as_float(c[i]) + __uint_as_float(d[i]);
+                    p = __float_as_uint(begun ? __uint_as_float(p) + sum : sum);
+                }
+                c[i] = d[i] = 0;
+            }
+            begun = true;
+        };
+        int left = kSegment;
         do {                                           // the loads of the next step, or unit, go ahead of the MMAs
             uint4 cl[4], ch[4], cb[4];
 #pragma unroll
@@ -160,14 +180,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
                 small_mma<I8>(c, cl[u].x, ch[u].x, cl[u].y, ch[u].y, cb[u].x, cb[u].y, a.f16);
                 small_mma<I8>(d, cl[u].z, ch[u].z, cl[u].w, ch[u].w, cb[u].z, cb[u].w, a.f16);
             }
+            if (!I8 && --left == 0 && k0 < a.k_bytes) {
+                fold();
+                left = kSegment;
+            }
         } while (k0 < a.k_bytes);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            c[i] = I8 ? c[i] + d[i] : __float_as_uint(__uint_as_float(c[i]) + __uint_as_float(d[i]));
-        part[warp][2 * t][g] = c[0];
-        part[warp][2 * t + 1][g] = c[1];
-        part[warp][2 * t][g + 8] = c[2];
-        part[warp][2 * t + 1][g + 8] = c[3];
+        fold();
         __syncthreads();
         const int col = threadIdx.x / kSmallRows, f = cur.f0 + threadIdx.x % kSmallRows;
         if (col < kSmallTok && cur.tok + col < cur.hi && f < a.M) {

@@ -1,0 +1,90 @@
+"""How exact the sums of the experts' products are, with operands of one sign.
+
+There the sum of the absolute values is the result itself, so a bias towards
+zero cannot hide behind terms that cancel.  Operands lie in [1, 1.25]: products
+in [1, 25/16], and a partial sum of i MMAs of 16 terms is at most 25 i.
+
+What a tensor core loses (its alignment, seen by adding 15 equal terms to one
+2^k times as large: whole down to 2^-25 of it, partly or wholly gone from 2^-26 on): each MMA
+lines its addends up with the largest partial sum P and cuts each at or below
+2^-25 P, 16 of them 4 * 2^-23 P together, and then cuts the sum to fp32, 2^-23 P,
+all towards zero.  In bf16 the products are multiples of 2^-14 and no segment of
+512 terms reaches 2^10, whose addends are cut at 2^-16: only the sum's cut is
+left.  So an MMA loses at most c 2^-23 P with c = 1 (bf16) or 5 (fp16), a segment of
+m MMAs at most c 2^-23 25 m (m + 1) / 2, and n terms in segments of m MMAs at most
+c 2^-23 (25 / 32) (m + 1) n.
+
+Adding the segments up rounds to nearest, each time at most 2^-24 of what has
+been added so far: J in a row cost at most 2^-24 (25 / 16) (J + 1) / 2 of the sum,
+and a few more for the parts of a block, a pair or a pair of accumulators.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_43_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+T = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+MOE = {"bf16": B.MOE_DTYPE_BF16, "f16": B.MOE_DTYPE_F16, "f32": B.MOE_DTYPE_F32}
+CUTS = {"bf16": 1, "f16": 5}                      # c above
+MMAS = 32                                         # MMAs of a segment, at most
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def _above_one(shape, dtype, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return (1 + torch.rand(shape, generator=gen, device="cuda") / 4).to(T[dtype])
+
+
+def _offsets(counts):
+    return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+
+
+def _done():
+    torch.cuda.synchronize()
+    assert B.moe_grouped_status() == B.MOE_OK
+
+
+def _product64(a, b):
+    """a [m][n] times b [o][n], transposed, in 64 bits."""
+    out = torch.zeros((a.shape[0], b.shape[0]), dtype=torch.float64, device="cuda")
+    for i in range(0, a.shape[1], 1 << 16):
+        out += a[:, i:i + (1 << 16)].double() @ b[:, i:i + (1 << 16)].double().T
+    return out
+
+
+def _bound(n, ref, dtype, joins, more):
+    return CUTS[dtype] * 2.0 ** -23 * (25 / 32) * (MMAS + 1) * n + ref * 2.0 ** -24 * ((25 / 16) * (joins + 1) / 2 + more)
+
+
+def gemm(counts, d_in, d_out, dtype, out, seed=1):
+    E, R = len(counts), sum(counts)
+    off = _offsets(counts)
+    x, w = _above_one((R, d_in), dtype, seed), _above_one((E, d_out, d_in), dtype, seed + 1)
+    y = torch.empty((R, d_out), dtype=T[out], device="cuda")
+    B.moe_grouped_gemm(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], MOE[out], 0, off.data_ptr(), d_in, d_out),
+                       x.data_ptr(), w.data_ptr(), y.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _done()
+    ends = off.tolist()
+    ref = torch.cat([_product64(x[a:b], w[e]) for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))])
+    return y, ref
+
+
+# few rows: a block's eight warps share the reduction, each adding its two accumulators to its part of the sum after
+# every segment: a join for each 8 steps of 1024 terms, the accumulators' own and the warps' 8
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,d_in,d_out", [([1], 1024, 64), ([2, 0, 1], 8192 + 8, 24), ([3, 1], 65536, 40),
+                                               ([0, 2], (1 << 18) - 8, 16), ([1, 1], 1 << 20, 8)], ids=str)
+def test_few_rows_of_any_length(counts, d_in, d_out, dtype):
+    y, ref = gemm(counts, d_in, d_out, dtype, "f32")
+    tol = _bound(d_in, ref, dtype, joins=-(-d_in // 8192), more=1 + 8 + 1)
+    err = (y.double() - ref).abs()
+    assert bool((err <= tol).all()), f"{(err / ref).max().item():.3g} of the sum, {(tol / ref).max().item():.3g} allowed"
