@@ -444,8 +444,10 @@ typedef struct moe_grouped {
 } moe_grouped_t;
 
 /* y[r] = W[e] x[r] for the rows r of each expert e: x [rows][d_in],
- * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once (an F32
- * result is within about 1e-6 of the sum).  Every row's result depends on its
+ * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once.  An F32
+ * result is within about 1e-6 of the sum of its terms' absolute values: the tensor
+ * cores' sums, which are cut and not rounded, are added up in short segments (over
+ * millions of terms the roundings of that addition reach 3e-6).  Every row's result depends on its
  * own x and its expert's weights alone. */
 moe_status_t moe_grouped_gemm(const moe_grouped_t* g, const void* x, const void* w, void* y,
                               void* stream);

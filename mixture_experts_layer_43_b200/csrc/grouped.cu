@@ -50,6 +50,8 @@ static __device__ uint32_t g_grouped_err;
 
 namespace {
 
+#include "grouped_small.cuh"
+
 constexpr int kMaxDevices = 64;
 constexpr int kTile = 256;                        // tile rows (M), and the most columns (N)
 constexpr int kHalf = 128;                        // rows of the tile one CTA holds
@@ -57,14 +59,16 @@ constexpr int kKBytes = 128;                      // k-step: 64 16-bit or 128 8-
 constexpr int kStageHalf = kHalf * kKBytes;       // 16 KB, of A and of B
 constexpr int kStage = 2 * kStageHalf;
 constexpr int kStages = 6;
-// An fp32 result is summed in segments of this many k-steps (512 terms), which
-// the epilogue adds up: the tensor core cuts its accumulator to fp32 after each
-// 16 terms, always towards zero, which over a long reduction costs more than
-// roundings to nearest (measured over 1024 rows: 1.0e-6 of the result in one
-// sum).  A 16-bit result does not show it.
-constexpr int kSegment = 8;
-
-#include "grouped_small.cuh"
+// An fp32 result is summed in segments of so many k-steps of 64 terms, which the
+// epilogue adds up in fp32 rounded to nearest.  The tensor core lines up the 16
+// terms of an MMA with the accumulator P, cuts them at 2^-25 P and the sum to fp32,
+// always towards zero, which over a long reduction costs more than roundings to
+// nearest.  Products of bf16 have 16 significant bits and mostly fit: 512 terms of
+// one sign lose 7e-7 of their sum.  Products of fp16 have up to 22, and the cut
+// terms add their share: 2.5e-6 in 512 terms, 1.1e-6 in 256, 4.6e-7 in 128.  The
+// shorter segments cost 3 to 12% (DeepSeek-shaped dgrad with an fp32 result 268 us
+// with 512, 275 with 256, 293 to 317 with 128).  A 16-bit result does not show it.
+constexpr int kSegment = 8, kSegmentF16 = 2;
 
 constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
 constexpr int kEpiWarps = 8;                      // two for each quarter of the TMEM lanes
@@ -83,6 +87,7 @@ struct TcArgs {
     int M, N;              // M: output features (wgrad: d_in).  N: wgrad's columns (d_out)
     int nk;                // k-steps of gemm and dgrad
     int split;             // pairs of a tile (SPLIT)
+    int segment;           // k-steps of a segment (F32)
     int m_block;           // gemm, dgrad: weight tiles of a block (see TileWalk)
     int out_dtype, accumulate;
     uint32_t idesc;        // without the N field
@@ -564,7 +569,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                     wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + b * kTile;
-                    const int end = F32 ? min(kb + kSegment, g.k_to) : g.k_to, k0 = kb;
+                    const int end = F32 ? min(kb + a.segment, g.k_to) : g.k_to, k0 = kb;
                     for (; kb < min(end, n_full); ++kb) {
                         wait(full_u + s * 8, phase);
                         tc_fence_after();
@@ -642,7 +647,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
                 const bool none = g.k_from == g.k_to;
                 const int segments =
-                    empty_expert ? 0 : F32 && !none ? (g.k_to - g.k_from + kSegment - 1) / kSegment : 1;
+                    empty_expert ? 0 : F32 && !none ? (g.k_to - g.k_from + a.segment - 1) / a.segment : 1;
                 for (int seg = 0; seg < segments; ++seg, ++local) {
                     const int b = local & 1;
                     // every decision before the warp-collective tcgen05.ld is warp-uniform
@@ -950,6 +955,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         const size_t n = static_cast<size_t>(c.E) * c.d_out * c.d_in * (c.out_dtype == MOE_DTYPE_F32 ? 4 : 2);
         return cudaMemsetAsync(c.out, 0, n, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
+    const int segment = c.dtype == MOE_DTYPE_F16 && c.out_dtype == MOE_DTYPE_F32 ? kSegmentF16 : kSegment;
     if (op == kOpGemm && few_rows(c)) {
         SmallArgs m{};
         m.offsets = c.offsets;
@@ -966,6 +972,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
         m.k_bytes = c.d_in * elem;
         m.f16 = c.dtype == MOE_DTYPE_F16;
         m.out_dtype = c.out_dtype;
+        m.segment = segment;
         const int64_t units = ceil_div(c.d_out, kSmallRows) * (c.rows < c.E ? c.rows : c.E);    // at most
         const unsigned grid = static_cast<unsigned>(units < 2 * 148 ? units : 2 * 148);
         const cudaError_t e = launch_chained(i8 ? grouped_small_kernel<true> : grouped_small_kernel<false>, dim3(grid),
@@ -982,6 +989,7 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
     a.E = c.E;
     a.out_dtype = c.out_dtype;
     a.accumulate = c.accumulate;
+    a.segment = segment;
     // D fp32 (int32), A and B bf16 (signed 8-bit; fp16 is 0), M 256 over the pair
     a.idesc = (i8 ? 2u << 4 : 1u << 4) | (16u << 24);
     if (c.dtype != MOE_DTYPE_F16) a.idesc |= (1u << 7) | (1u << 10);

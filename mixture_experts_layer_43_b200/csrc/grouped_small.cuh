@@ -13,9 +13,9 @@
 // through shared memory but the eight warps' partial sums (added in order; two
 // sets of them, so that a piece costs one barrier).  Over a long reduction a warp
 // adds its accumulators to its partial sum, in fp32 rounded to nearest, after each
-// kSegment steps and starts them anew: like a tile's accumulator, they lose up to
-// a unit of fp32 with every MMA, always towards zero (65536 terms in one sum: 1.1e-5
-// of the result in bf16, 2.4e-5 in fp16).
+// segment (of 64 terms a step in each accumulator, as long as a tile's) and starts
+// them anew: they lose some of the sum with every MMA, always towards zero (65536
+// terms in one sum: 1.1e-5 of the result in bf16, 2.4e-5 in fp16).
 //
 // Two blocks an SM keep 128 KB of weights in flight: 16 rows through 8 experts of
 // 14336 x 4096 (fp16) take 135 us, 6.1 TB/s; one row through 4096 x 4096 8.0 us, of
@@ -41,6 +41,7 @@ struct SmallArgs {
     int64_t rows;
     int E, M, k_bytes;                          // M: output features
     int f16, out_dtype;
+    int segment;                                // steps of a segment
 };
 
 template <bool I8>
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
             }
             begun = true;
         };
-        int left = kSegment;
+        int left = a.segment;
         do {                                           // the loads of the next step, or unit, go ahead of the MMAs
             uint4 cl[4], ch[4], cb[4];
 #pragma unroll
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) grouped_small_kernel(const S
             }
             if (!I8 && --left == 0 && k0 < a.k_bytes) {
                 fold();
-                left = kSegment;
+                left = a.segment;
             }
         } while (k0 < a.k_bytes);
         fold();

@@ -88,3 +88,62 @@ def test_few_rows_of_any_length(counts, d_in, d_out, dtype):
     tol = _bound(d_in, ref, dtype, joins=-(-d_in // 8192), more=1 + 8 + 1)
     err = (y.double() - ref).abs()
     assert bool((err <= tol).all()), f"{(err / ref).max().item():.3g} of the sum, {(tol / ref).max().item():.3g} allowed"
+
+
+# In earnest: segments of 512 terms in bf16 and of 128 in fp16.  A cut loses half of its most on average, and 2^-23 P
+# stands for one unit of fp32, which is 0.72 of that on average over P's significand: 0.36 2^-23 P for the sum and, where
+# every bit of the terms is at stake, 1.44 2^-23 P for the 16 of them.  Segments of m MMAs of even terms then lose
+# (m + 1) / 2 times as much of their sum: 16.5 * 0.36 * 2^-23 = 7.1e-7 in bf16 and 4.5 * 1.8 * 2^-23 = 9.7e-7 in fp16,
+# on average over the elements.
+def _average(y, ref):
+    return ((y.double() - ref) / ref).mean().abs().item()
+
+
+# one pair a tile; two and four pairs that share a reduction; few rows; ends inside a k-step
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,d_in,d_out", [([300], 1024, 4104), ([300], 8192 + 8, 4104), ([64], 8192, 4096 + 8),
+                                               ([40, 0, 30], 65536, 264), ([2, 1], 1024, 264), ([1, 3], 65536, 40)], ids=str)
+def test_gemm_in_32_bits(counts, d_in, d_out, dtype):
+    y, ref = gemm(counts, d_in, d_out, dtype, "f32", seed=5)
+    err, tol = (y.double() - ref).abs(), _bound(d_in, ref, dtype, joins=-(-d_in // 128), more=10)
+    assert bool((err <= tol).all()), f"{(err / ref).max().item():.3g} of the sum"
+    assert _average(y, ref) <= 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,d_in,d_out", [([300, 21], 4104, 1024), ([64], 264, 65536)], ids=str)
+def test_dgrad_in_32_bits(counts, d_in, d_out, dtype):
+    E, R, off = len(counts), sum(counts), _offsets(counts)
+    dy, w = _above_one((R, d_out), dtype, 7), _above_one((E, d_out, d_in), dtype, 8)
+    dx = torch.empty((R, d_in), device="cuda")
+    B.moe_grouped_dgrad(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], 2, 0, off.data_ptr(), d_in, d_out),
+                        dy.data_ptr(), w.data_ptr(), dx.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _done()
+    ends = off.tolist()
+    ref = torch.cat([_product64(dy[a:b], w[e].T) for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))])
+    err, tol = (dx.double() - ref).abs(), _bound(d_out, ref, dtype, joins=-(-d_out // 128), more=10)
+    assert bool((err <= tol).all()), f"{(err / ref).max().item():.3g} of the sum"
+    assert _average(dx, ref) <= 1e-6
+
+
+def wgrad(counts, d_in, d_out, dtype, out, accumulate=0):
+    E, R, off = len(counts), sum(counts), _offsets(counts)
+    dy, x = _above_one((R, d_out), dtype, 9), _above_one((R, d_in), dtype, 10)
+    dw = torch.zeros((E, d_out, d_in), dtype=T[out], device="cuda")
+    B.moe_grouped_wgrad(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], MOE[out], accumulate, off.data_ptr(), d_in, d_out),
+                        dy.data_ptr(), x.data_ptr(), dw.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _done()
+    ends = off.tolist()
+    return dw, torch.stack([_product64(dy[a:b].T, x[a:b].T) for a, b in zip(ends[:-1], ends[1:])])
+
+
+# many tiles; a few that pairs share; accumulated
+@pytest.mark.parametrize("acc", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,d_in,d_out", [([1000, 8200], 1032, 2056), ([8200], 264, 72), ([70001], 64, 264)], ids=str)
+def test_wgrad_in_32_bits(counts, d_in, d_out, dtype, acc):
+    dw, ref = wgrad(counts, d_in, d_out, dtype, "f32", acc)
+    for e, n in enumerate(counts):
+        err, tol = (dw[e].double() - ref[e]).abs(), _bound(n, ref[e], dtype, joins=-(-n // 128), more=10)
+        assert bool((err <= tol).all()), f"{(err / ref[e]).max().item():.3g} of the sum"
+        assert _average(dw[e], ref[e]) <= 1e-6
