@@ -67,8 +67,15 @@ constexpr int kStages = 6;
 // one sign lose 7e-7 of their sum.  Products of fp16 have up to 22, and the cut
 // terms add their share: 2.5e-6 in 512 terms, 1.1e-6 in 256, 4.6e-7 in 128.  The
 // shorter segments cost 3 to 12% (DeepSeek-shaped dgrad with an fp32 result 268 us
-// with 512, 275 with 256, 293 to 317 with 128).  A 16-bit result does not show it.
+// with 512, 275 with 256, 293 to 317 with 128).
 constexpr int kSegment = 8, kSegmentF16 = 2;
+// A 16-bit result shows it only over long reductions: n terms of one sign in one
+// sum lose 4.8e-9 n of it in fp16 (measured, 2^17 to 2^22 terms: 2.1e-4 to 6.9e-3)
+// and 8e-10 n in bf16 (6.8e-5 to 5.2e-3).  Reductions that may be longer than these
+// limits, where that is a third and a fifth of half a step (2^-11, 2^-8), go in
+// segments of kSegment steps, too (49152 fp16 rows of 64 experts of 2048 x 2816:
+// weight gradient 553 us with them, 523 without).
+constexpr int64_t kLongF16 = 1 << 15, kLongBf16 = 1 << 20;
 
 constexpr int kBoxRows = 32;                      // rows of one TMA box of the N side
 constexpr int kEpiWarps = 8;                      // two for each quarter of the TMEM lanes
@@ -87,7 +94,7 @@ struct TcArgs {
     int M, N;              // M: output features (wgrad: d_in).  N: wgrad's columns (d_out)
     int nk;                // k-steps of gemm and dgrad
     int split;             // pairs of a tile (SPLIT)
-    int segment;           // k-steps of a segment (F32)
+    int segment;           // k-steps of a segment (SEG)
     int m_block;           // gemm, dgrad: weight tiles of a block (see TileWalk)
     int out_dtype, accumulate;
     uint32_t idesc;        // without the N field
@@ -405,11 +412,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-// F32: 16-bit operands with an fp32 result, summed in segments (see kSegment).
+// SEG: 16-bit operands summed in segments (see kSegment), for fp32 results and long
+// reductions.
 // SPLIT: a.split pairs (a cluster of 2 a.split CTAs, one tile each) take parts
 // of a tile's reduction and trade their sums through distributed shared memory,
 // each adding up (in a fixed order) and storing its share of the columns.
-template <int OP, bool I8, bool F32, bool SPLIT>
+template <int OP, bool I8, bool SEG, bool SPLIT>
 __global__ void __launch_bounds__(tc_threads<OP>(), 1)
 grouped_tc_kernel(const __grid_constant__ TcArgs a) {
     constexpr int kElem = I8 ? 1 : 2;
@@ -569,7 +577,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                     wait(tempty_u + b * 8, ((local >> 1) & 1) ^ 1);
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + b * kTile;
-                    const int end = F32 ? min(kb + a.segment, g.k_to) : g.k_to, k0 = kb;
+                    const int end = SEG ? min(kb + a.segment, g.k_to) : g.k_to, k0 = kb;
                     for (; kb < min(end, n_full); ++kb) {
                         wait(full_u + s * 8, phase);
                         tc_fence_after();
@@ -636,7 +644,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
             auto scale_of = [&](int c) {                      // 8 bits: of this lane's token of column c ..
                 return I8 && c + lane < valid ? a.a_scale[col0 + c + lane] : 0.f;
             };
-            if constexpr (F32 || SPLIT) {
+            if constexpr (SEG || SPLIT) {
                 // the segments' sums are added up here, in fp32 rounded to nearest
                 // (8 bits: one segment, whose words are int32)
                 const int part = first_part;
@@ -647,7 +655,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
                 const bool none = g.k_from == g.k_to;
                 const int segments =
-                    empty_expert ? 0 : F32 && !none ? (g.k_to - g.k_from + a.segment - 1) / a.segment : 1;
+                    empty_expert ? 0 : SEG && !none ? (g.k_to - g.k_from + a.segment - 1) / a.segment : 1;
                 for (int seg = 0; seg < segments; ++seg, ++local) {
                     const int b = local & 1;
                     // every decision before the warp-collective tcgen05.ld is warp-uniform
@@ -664,7 +672,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
-                                    sum[j][h * 16 + i] = F32 ? sum[j][h * 16 + i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+                                    sum[j][h * 16 + i] = SEG ? sum[j][h * 16 + i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
                             }
                         }
                     }
@@ -713,7 +721,7 @@ grouped_tc_kernel(const __grid_constant__ TcArgs a) {
                             }
                         }
                     }
-                    if constexpr (F32) {
+                    if (SEG && a.out_dtype == MOE_DTYPE_F32) {
                         if (f >= a.M) break;
                         float* o = static_cast<float*>(a.out) + (col0 + c) * a.out_stride + f;
                         if (OP == kOpWgrad && a.accumulate) {
@@ -854,9 +862,9 @@ bool stack_map(CUtensorMap* m, int elem, const void* base, int64_t cols, int64_t
 
 // Once per device: raise the kernels' shared-memory limit and ask how many
 // pairs fit.
-template <int OP, bool I8, bool F32, bool SPLIT>
+template <int OP, bool I8, bool SEG, bool SPLIT>
 bool prepare_kernel(int* pairs) {
-    auto* k = grouped_tc_kernel<OP, I8, F32, SPLIT>;
+    auto* k = grouped_tc_kernel<OP, I8, SEG, SPLIT>;
     const int smem = static_cast<int>(tc_smem_bytes<OP>(kMaxExperts));
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
     // clusters of 8 are within the portable size: nothing more to ask for
@@ -876,9 +884,9 @@ bool prepare_kernel(int* pairs) {
     return true;
 }
 
-template <int OP, bool I8, bool F32>
+template <int OP, bool I8, bool SEG>
 bool prepare_kernels(int* pairs) {
-    return prepare_kernel<OP, I8, F32, false>(pairs) && prepare_kernel<OP, I8, F32, true>(pairs);
+    return prepare_kernel<OP, I8, SEG, false>(pairs) && prepare_kernel<OP, I8, SEG, true>(pairs);
 }
 
 int device_pairs() {
@@ -912,7 +920,7 @@ int pick_split(int64_t tiles, int nk, int cols) {
     return tiles <= 13 ? 4 : tiles <= 32 ? 2 : 1;
 }
 
-template <int OP, bool I8, bool F32>
+template <int OP, bool I8, bool SEG>
 moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t stream) {
     const int pairs = device_pairs();
     if (!pairs) return MOE_ERR_CUDA;
@@ -920,8 +928,8 @@ moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t 
     const dim3 grid(2 * static_cast<unsigned>(a.split > 1 ? tiles * a.split : tiles < pairs ? tiles : pairs));
     const size_t smem = tc_smem_bytes<OP>(a.E);
     const cudaError_t e =
-        a.split > 1 ? launch_chained(grouped_tc_kernel<OP, I8, F32, true>, grid, tc_threads<OP>(), smem, 2 * a.split, stream, a)
-                    : launch_chained(grouped_tc_kernel<OP, I8, F32, false>, grid, tc_threads<OP>(), smem, 2, stream, a);
+        a.split > 1 ? launch_chained(grouped_tc_kernel<OP, I8, SEG, true>, grid, tc_threads<OP>(), smem, 2 * a.split, stream, a)
+                    : launch_chained(grouped_tc_kernel<OP, I8, SEG, false>, grid, tc_threads<OP>(), smem, 2, stream, a);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1036,7 +1044,8 @@ moe_status_t launch_grouped(GroupedOp op, const GroupedCall& c, cudaStream_t str
     }
     if (!ok || tiles > 0x7FFF0000) return MOE_ERR_INVALID_ARG;
     if (i8) return launch_tc<kOpGemm, true, false>(a, tiles, nk, cols, stream);
-    if (c.out_dtype == MOE_DTYPE_F32) {
+    const int64_t terms = op == kOpGemm ? c.d_in : op == kOpDgrad ? c.d_out : c.rows;        // of a sum, at most
+    if (c.out_dtype == MOE_DTYPE_F32 || terms > (c.dtype == MOE_DTYPE_F16 ? kLongF16 : kLongBf16)) {
         if (op == kOpGemm) return launch_tc<kOpGemm, false, true>(a, tiles, nk, cols, stream);
         if (op == kOpDgrad) return launch_tc<kOpDgrad, false, true>(a, tiles, nk, cols, stream);
         return launch_tc<kOpWgrad, false, true>(a, tiles, nk, cols, stream);

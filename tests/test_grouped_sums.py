@@ -65,10 +65,10 @@ def _bound(n, ref, dtype, joins, more):
     return CUTS[dtype] * 2.0 ** -23 * (25 / 32) * (MMAS + 1) * n + ref * 2.0 ** -24 * ((25 / 16) * (joins + 1) / 2 + more)
 
 
-def gemm(counts, d_in, d_out, dtype, out, seed=1):
+def gemm(counts, d_in, d_out, dtype, out, seed=1, scale=1.0):
     E, R = len(counts), sum(counts)
     off = _offsets(counts)
-    x, w = _above_one((R, d_in), dtype, seed), _above_one((E, d_out, d_in), dtype, seed + 1)
+    x, w = _above_one((R, d_in), dtype, seed) * scale, _above_one((E, d_out, d_in), dtype, seed + 1) * scale
     y = torch.empty((R, d_out), dtype=T[out], device="cuda")
     B.moe_grouped_gemm(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], MOE[out], 0, off.data_ptr(), d_in, d_out),
                        x.data_ptr(), w.data_ptr(), y.data_ptr(), torch.cuda.current_stream().cuda_stream)
@@ -126,9 +126,9 @@ def test_dgrad_in_32_bits(counts, d_in, d_out, dtype):
     assert _average(dx, ref) <= 1e-6
 
 
-def wgrad(counts, d_in, d_out, dtype, out, accumulate=0):
+def wgrad(counts, d_in, d_out, dtype, out, accumulate=0, scale=1.0):
     E, R, off = len(counts), sum(counts), _offsets(counts)
-    dy, x = _above_one((R, d_out), dtype, 9), _above_one((R, d_in), dtype, 10)
+    dy, x = _above_one((R, d_out), dtype, 9) * scale, _above_one((R, d_in), dtype, 10) * scale
     dw = torch.zeros((E, d_out, d_in), dtype=T[out], device="cuda")
     B.moe_grouped_wgrad(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], MOE[out], accumulate, off.data_ptr(), d_in, d_out),
                         dy.data_ptr(), x.data_ptr(), dw.data_ptr(), torch.cuda.current_stream().cuda_stream)
@@ -147,3 +147,37 @@ def test_wgrad_in_32_bits(counts, d_in, d_out, dtype, acc):
         err, tol = (dw[e].double() - ref[e]).abs(), _bound(n, ref[e], dtype, joins=-(-n // 128), more=10)
         assert bool((err <= tol).all()), f"{(err / ref[e]).max().item():.3g} of the sum"
         assert _average(dw[e], ref[e]) <= 1e-6
+
+
+# Results of 16 bits: a reduction long enough for the cuts to show in half a step of the result goes in segments, too
+def _close16(got, ref, n, dtype, joins):
+    info = torch.finfo(T[dtype])
+    tol = _bound(n, ref, dtype, joins, more=10)
+    tol = tol + (ref + tol) * (info.eps / 2) + info.smallest_normal * info.eps / 2
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), f"{(err / ref).max().item():.3g} of the sum, half a step is {info.eps / 2:.3g}"
+
+
+@pytest.mark.parametrize("counts,d_in,d_out,dtype", [([1 << 18], 40, 24, "f16"), ([70001, 0, 5, 200000], 264, 136, "f16"),
+                                                     ([(1 << 22) + 3], 16, 8, "bf16")], ids=str)
+def test_wgrad_of_millions_of_rows_in_16_bits(counts, d_in, d_out, dtype):
+    # by 2^-8 each, exact: sums of 2^18 products stay in fp16's range
+    dw, ref = wgrad(counts, d_in, d_out, dtype, dtype, scale=2.0 ** -8)
+    for e, n in enumerate(counts):
+        _close16(dw[e], ref[e], n * 2.0 ** -16, dtype, joins=-(-n // 512))
+
+
+@pytest.mark.parametrize("counts,d_in,d_out", [([64], (1 << 20) - 8, 16), ([20, 0, 44], 1 << 19, 264), ([2], 1 << 20, 8)], ids=str)
+def test_long_products_in_fp16(counts, d_in, d_out):
+    y, ref = gemm(counts, d_in, d_out, "f16", "f16", scale=2.0 ** -8)
+    _close16(y, ref, d_in * 2.0 ** -16, "f16", joins=-(-d_in // 512))
+
+
+def test_long_dgrad_in_fp16():
+    R, d_in, d_out, off = 50, 24, 1 << 20, _offsets([50])
+    dy, w = _above_one((R, d_out), "f16", 11) * 2.0 ** -8, _above_one((1, d_out, d_in), "f16", 12) * 2.0 ** -8
+    dx = torch.empty((R, d_in), dtype=torch.float16, device="cuda")
+    B.moe_grouped_dgrad(B.moe_grouped_t(R, 1, d_in, d_out, 1, 1, 0, off.data_ptr(), d_in, d_out),
+                        dy.data_ptr(), w.data_ptr(), dx.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _done()
+    _close16(dx, _product64(dy, w[0].T), d_out * 2.0 ** -16, "f16", joins=-(-d_out // 512))
