@@ -12,19 +12,21 @@ namespace {
 constexpr int kRowThreads = 256;
 
 template <bool F16>
+__device__ __forceinline__ void unpack2(uint32_t w, float (&f)[2]) {
+    if (F16) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        f[0] = p.x;
+        f[1] = p.y;
+    } else {
+        f[0] = __uint_as_float(w << 16);
+        f[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+}
+template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (F16) {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            f[2 * i] = p.x;
-            f[2 * i + 1] = p.y;
-        } else {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
+    for (int i = 0; i < 4; ++i) unpack2<F16>(w[i], reinterpret_cast<float (&)[2]>(f[2 * i]));
 }
 template <bool F16>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
@@ -40,8 +42,9 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret
 // the rounding of t alone would cost |g| half steps of the result: 2^t =
 // 2^hi (1 + lo ln 2).  Errors in units of 2^-24: 2^hi 4 (ex2.approx), 1 + lo
 // ln 2 and the product 1 each, 1 + 2^t 1, the reciprocal 2: at most 9.  Below
-// g = -87.3 the result is under 2^-126 and taken as 0.  At an infinity lo is NaN:
-// fminf drops it (the factor is never above 1.0001 otherwise).
+// g = -87.3 the result is under 2^-126 and comes out as 0 (sigmoid_tail has those).
+// At an infinity lo is NaN: fminf drops it (the factor is never above 1.0001
+// otherwise).
 __device__ __forceinline__ float sigmoid_f(float g) {
     constexpr float kL = -1.44269504f, kLlo = -1.92596299e-8f, kLn2 = 0.693147181f;
     const float hi = g * kL;
@@ -51,6 +54,74 @@ __device__ __forceinline__ float sigmoid_f(float g) {
     p *= fminf(fmaf(lo, kLn2, 1.f), 1.0001f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
     return r;
+}
+
+// (g + plus) sig(g) b for gates whose sigmoid is below the smallest normal number
+// while its product with g and b need not be: there sig(g) = e^g = q 2^-n with q near
+// 1, and the powers of two are multiplied in behind g and b, a normal number at a
+// time.  Gates of -300 and below give 0 with every finite b (e^-300 < 2^-432).
+constexpr float kTail = -87.f, kTailEnd = -300.f;
+__device__ __forceinline__ bool in_tail(float g) { return g < kTail && g > kTailEnd; }
+__device__ __forceinline__ float sigmoid_tail(float g, float plus, float b) {
+    constexpr float kL = -1.44269504f, kLlo = -1.92596299e-8f, kLn2 = 0.693147181f;
+    const float hi = g * kL;
+    const float lo = fmaf(g, kLlo, fmaf(g, kL, -hi));
+    const float whole = rintf(hi);
+    float q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(whole - hi));
+    q *= fmaf(lo, -kLn2, 1.f);
+    int n = static_cast<int>(whole);
+    float v = (g + plus) * q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                      // n <= 433
+        const int k = min(n, 126);
+        v *= __int_as_float((127 - k) << 23);
+        if (i == 0) v *= b;
+        n -= k;
+    }
+    return v;
+}
+// Whether one of 8 gates is below kTail, by the maximum of their bits: negative
+// 16-bit numbers order by them, above the positive ones (a negative NaN passes, too).
+template <bool F16>
+__device__ __forceinline__ bool any_tail(const uint4& v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x, v.y), __vmaxu2(v.z, v.w));
+    return max(m & 0xFFFFu, m >> 16) > (F16 ? 0xD570u : 0xC2AEu);
+}
+// The words of a vector move up one place.
+__device__ __forceinline__ void turn(uint4& v, uint32_t last) { v = make_uint4(v.y, v.z, v.w, last); }
+
+// f = g sig(g) u of 8 values.  A vector with a gate in the tail is rare and takes a
+// loop over its words, which keeps the kernels' registers as they are without it
+// (a branch behind the common path took 40 instead of 32 in SwiGLU, 58 in its
+// gradient).  The look at the gates costs nothing measurable there (24576 x 1408
+// bf16: 31.0 us, gradient 52.0) and 2.3 us of 42 where codes follow; one look for
+// all of a thread's vectors, with a second pass, cost 9.5.
+template <bool F16>
+__device__ __forceinline__ void glu8(uint4 gate, uint4 up, float (&f)[8]) {
+    if (any_tail<F16>(gate)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+            float g[2], u[2];
+            unpack2<F16>(gate.x, g);
+            unpack2<F16>(up.x, u);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) f[i] = f[i + 2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                f[6 + i] = in_tail(g[i]) ? sigmoid_tail(g[i], 0.f, u[i]) : g[i] * sigmoid_f(g[i]) * u[i];
+            turn(gate, 0);
+            turn(up, 0);
+        }
+        return;
+    }
+    float u[8];
+    unpack8<F16>(gate, f);
+    unpack8<F16>(up, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid_f(f[i]) * u[i];
 }
 
 // Vector i of `n` as a row and a first column, for fewer than 2^31 vectors:
@@ -90,16 +161,27 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(const RowsCall c, c
         int col;
         place<BIG>(i, f, r, col);
         const uint4 vg = load16(gate + r * c.in_stride + col), vu = load16(up + r * c.in_stride + col);
-        float g[8], u[8];
-        unpack8<F16>(vg, g);
-        unpack8<F16>(vu, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = g[j] * sigmoid_f(g[j]) * u[j];
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + r * c.out_stride + col) = pack8<F16>(g);
+        float h[8];
+        glu8<F16>(vg, vu, h);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + r * c.out_stride + col) = pack8<F16>(h);
     }
 }
 
-// dgate = dh u sig(g) (1 + g (1 - sig(g))),  dup = dh g sig(g)
+// dgate = dh u sig(g) (1 + g (1 - sig(g))),  dup = dh g sig(g), in the place of g and u
+template <bool TAIL>
+__device__ __forceinline__ void grad_of(float& g, float& u, float d) {
+    if (TAIL && in_tail(g)) {                          // 1 - sig(g) is 1
+        const float dg = sigmoid_tail(g, 1.f, d * u);
+        u = sigmoid_tail(g, 0.f, d);
+        g = dg;
+        return;
+    }
+    const float s = sigmoid_f(g);
+    const float t = d * s;
+    const float dg = t * u * (1.f + g * (1.f - s));
+    u = t * g;
+    g = dg;
+}
 template <bool F16, bool BIG>
 __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall c, const FastDiv f) {
     const int64_t n = c.rows * f.d;
@@ -115,20 +197,34 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_grad_kernel(const RowsCall
         place<BIG>(i, f, r, col);
         const uint4 vg = load16(gate + r * c.in_stride + col), vu = load16(up + r * c.in_stride + col);
         const uint4 vd = load16(dh + r * c.dh_stride + col);
+        uint16_t* dg = static_cast<uint16_t*>(c.out) + r * c.out_stride + col;
+        uint16_t* du = static_cast<uint16_t*>(c.out2) + r * c.out_stride + col;
+        if (any_tail<F16>(vg)) {                       // as in glu8
+            uint4 wg = vg, wu = vu, wd = vd;
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+                float g[2], u[2], d[2];
+                unpack2<F16>(wg.x, g);
+                unpack2<F16>(wu.x, u);
+                unpack2<F16>(wd.x, d);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) grad_of<true>(g[i], u[i], d[i]);
+                turn(wg, F16 ? pack_f16x2(g[0], g[1]) : pack_bf16x2(g[0], g[1]));
+                turn(wu, F16 ? pack_f16x2(u[0], u[1]) : pack_bf16x2(u[0], u[1]));
+                turn(wd, 0);
+            }
+            *reinterpret_cast<uint4*>(dg) = wg;
+            *reinterpret_cast<uint4*>(du) = wu;
+            continue;
+        }
         float g[8], u[8], d[8];
         unpack8<F16>(vg, g);
         unpack8<F16>(vu, u);
         unpack8<F16>(vd, d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s = sigmoid_f(g[j]);
-            const float t = d[j] * s;
-            const float dg = t * u[j] * (1.f + g[j] * (1.f - s));
-            u[j] = t * g[j];
-            g[j] = dg;
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + r * c.out_stride + col) = pack8<F16>(g);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out2) + r * c.out_stride + col) = pack8<F16>(u);
+        for (int j = 0; j < 8; ++j) grad_of<false>(g[j], u[j], d[j]);
+        *reinterpret_cast<uint4*>(dg) = pack8<F16>(g);
+        *reinterpret_cast<uint4*>(du) = pack8<F16>(u);
     }
 }
 
@@ -180,13 +276,6 @@ __global__ void __launch_bounds__(kRowThreads, GLU ? 4 : 5) i8_rows_kernel(const
     const uint16_t* pa = static_cast<const uint16_t*>(c.a) + (live ? r : 0) * c.in_stride;
     const uint16_t* pb = GLU ? static_cast<const uint16_t*>(c.b) + (live ? r : 0) * c.in_stride : nullptr;
 
-    auto glu = [&](const uint4& va, const uint4& vb, float (&f)[8]) {
-        float u[8];
-        unpack8<F16>(va, f);
-        unpack8<F16>(vb, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid_f(f[i]) * u[i];
-    };
     // |v| of 16-bit values order by their bits, two to an instruction
     uint32_t m = 0, m2 = 0;
     auto widen16 = [&](const uint4& v) {
@@ -212,7 +301,7 @@ __global__ void __launch_bounds__(kRowThreads, GLU ? 4 : 5) i8_rows_kernel(const
         for (int v = 0; v < VPT; ++v)
             if (t + v * TPR < vec) {
                 if constexpr (GLU) {
-                    glu(raw[v], raw_b[v], val[v]);
+                    glu8<F16>(raw[v], raw_b[v], val[v]);
                     widen(val[v]);
                 } else {
                     widen16(raw[v]);
@@ -221,7 +310,7 @@ __global__ void __launch_bounds__(kRowThreads, GLU ? 4 : 5) i8_rows_kernel(const
         for (int j = t + VPT * TPR; j < vec; j += TPR) {
             if constexpr (GLU) {
                 float f[8];
-                glu(load16(pa + j * 8), load16(pb + j * 8), f);
+                glu8<F16>(load16(pa + j * 8), load16(pb + j * 8), f);
                 widen(f);
             } else {
                 widen16(load16(pa + j * 8));
@@ -277,7 +366,7 @@ __global__ void __launch_bounds__(kRowThreads, GLU ? 4 : 5) i8_rows_kernel(const
         }
     for (int j = t + VPT * TPR; j < vec; j += TPR) {
         float f[8];
-        if constexpr (GLU) glu(load16(pa + j * 8), load16(pb + j * 8), f);
+        if constexpr (GLU) glu8<F16>(load16(pa + j * 8), load16(pb + j * 8), f);
         else unpack8<F16>(load16(pa + j * 8), f);
         store(j, f);
     }
