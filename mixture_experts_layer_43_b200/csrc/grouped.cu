@@ -37,6 +37,7 @@
 // once (977 MB); over half a second of such calls the power cap, not the kernel,
 // sets the time (244 us in a short run, 285 us sustained).
 #include <atomic>
+#include <cmath>
 
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -933,23 +934,31 @@ moe_status_t launch_tc(TcArgs& a, int64_t tiles, int nk, int cols, cudaStream_t 
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Whether a product goes to grouped_small_kernel.  Measured, small / tensor cores:
-//  - its 256-row weight tiles keep at most half of the CTA pairs busy, and its
-//    experts average at most 16 rows (a second pass over weights that L1 and L2
-//    hold): 8 experts of 2048 x 1024, a row each (32 tiles) 9.6 / 11.5 us; one of 4096
-//    x 4096 (16 tiles) with 1 row 8.0 / 13.1 us, with 16 rows 12.5 / 13.4; but 16
-//    experts of 2048 x 1024 (64 tiles) 18.6 / 14.9, 8 of 512 x 2048 (64) 9.2 / 7.2;
-//  - or its tiles are long (8192 weights a row) and make one to two waves, the
-//    second of which would leave pairs idle, and its experts average at most 2
-//    rows: 8 experts of 14336 x 4096 (128 tiles at most) with 8 rows 122 / 135 us, with
-//    16 rows 135 / 142, of 8192 x 4096 82 / 87, in 8 bits 77 / 82; but with 32 rows 181 /
-//    149, and 48 experts of 8192 x 1024 (192 tiles) 101 / 95, 8 of 4096 x 28672 (896
-//    tiles) 277 / 241.
+// Whether a product goes to grouped_small_kernel, which takes 8 rows of an expert in
+// a pass over its weights.  Measured in us, small / tensor cores, twelve sets of
+// weights in turn (so from HBM where one is above 10 MB), bf16 (8 bits alike at the
+// same bytes):
+//  - few tiles, one pass.  8 rows through 512 x 4096 (16 tiles) 3.7 / 5.4, 2048 x 4096
+//    6.9 / 10, 8192 x 4096 17 / 21; with 32 tiles 512 x 8192 6 / 6, 2048 x 8192 10.6 /
+//    12.1, but 4096 x 8192 18 / 17, 8192 x 8192 29 / 28 and with 24 tiles 8192 x 6144
+//    28 / 24, where two pairs share a tile.  One row costs what 8 do;
+//  - few tiles, two passes (10 to 16 rows of an expert).  The second reads the weights
+//    from L2: 2048 x 2048 (8 tiles) 8.2 / 9.1, 2048 x 4096 9.1 / 10, but 4096 x 4096 14.5 /
+//    13.6, 2048 x 8192 15.7 / 12.1, 8192 x 2048 21.6 / 14.6;
+//  - one to two waves of tiles, the second of which would leave most pairs idle.
+//    80 tiles: 4096 x 2560 38 / 42, 8192 x 2560 66 / 81, 14336 x 2560 110 / 131; 96 (six
+//    experts of 4096): 4096 45 / 43, 8192 79 / 81, 14336 131 / 135; but 112: 8192 90 / 82,
+//    14336 151 / 137; 128: 2048 30 / 24, 8192 95 / 88, 14336 158 / 148.  The call does not
+//    know how many experts have rows: the rule takes what even routing reaches.
 bool few_rows(const GroupedCall& c) {
     const int64_t slots = c.rows < c.E ? c.rows : c.E;      // experts with rows, at most
-    const int64_t tiles = slots * ceil_div(c.d_out, kTile);
-    if (tiles <= 37) return c.rows <= 16 * slots;
-    return tiles > 74 && tiles <= 148 && c.rows <= 2 * slots && c.d_in >= 8192;
+    const int64_t per_expert = ceil_div(c.d_out, kTile), tiles = slots * per_expert;
+    const int64_t k_bytes = static_cast<int64_t>(c.d_in) * (c.dtype == MOE_DTYPE_I8 ? 1 : 2);
+    if (tiles <= 16) return c.rows <= (k_bytes <= 4096 ? 16 : 8) * slots;
+    if (tiles <= 37) return k_bytes <= 4096 && c.rows <= 8 * slots;
+    if (tiles <= 74 || c.rows > 2 * slots || k_bytes < 8192) return false;
+    const double reached = c.E * (1 - std::pow(1 - 1.0 / c.E, static_cast<double>(c.rows))) * per_expert;
+    return reached > 74 && reached <= 100;
 }
 
 }  // namespace

@@ -17,10 +17,10 @@
 // them anew: they lose some of the sum with every MMA, always towards zero (65536
 // terms in one sum: 1.1e-5 of the result in bf16, 2.4e-5 in fp16).
 //
-// Two blocks an SM keep 128 KB of weights in flight: 16 rows through 8 experts of
-// 14336 x 4096 (fp16) take 135 us, 6.1 TB/s; one row through 4096 x 4096 8.0 us, of
-// which the bytes need 5.2.  Loading x ahead as well cost more in registers than it
-// hid (142 us, 8.6 us).
+// Two blocks an SM keep 64 KB of weights in flight (128 bytes a thread): 8 rows
+// through 8 experts of 14336 x 2560 take 110 us, 5.3 TB/s; one row through 4096 x 4096
+// 10.5 us from HBM, of which the bytes need 5.2.  Loading x ahead as well cost more in
+// registers than it hid (16 rows through 8 experts of 14336 x 4096 142 us, 135 without).
 #pragma once
 
 constexpr int kSmallThreads = 256;

@@ -181,3 +181,48 @@ def test_long_dgrad_in_fp16():
                         dy.data_ptr(), w.data_ptr(), dx.data_ptr(), torch.cuda.current_stream().cuda_stream)
     _done()
     _close16(dx, _product64(dy, w[0].T), d_out * 2.0 ** -16, "f16", joins=-(-d_out // 512))
+
+
+# The product of few rows by each of its rules, against 64 bits; random signs, so that the sums cancel: bounds as
+# in the tests of the tensor-core products, (n / 16 + 13) 2^-23 of the terms' absolute sum
+FEW = [
+    ([1], 4096, 4096),                               # a row, 16 tiles
+    ([8, 8], 8200, 2048),                            # one full pass, long
+    ([9, 16, 0, 1], 2048, 1032),                     # a second pass, full and of one row, short
+    ([21, 1, 0, 3, 0, 0, 1, 2], 264, 520),           # three passes of one expert, 24 tiles
+    ([2, 0, 1, 1, 0, 4, 0, 0], 8200, 4104),          # long tiles that would make two waves (8 rows, 136 tiles at most)
+    ([1] * 18 + [0] * 46, 8192, 1536),               # the same of many experts (108 tiles at most)
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("counts,d_in,d_out", FEW, ids=lambda v: str(v)[:24])
+def test_few_rows_by_every_rule(counts, d_in, d_out, dtype):
+    E, R, off = len(counts), sum(counts), _offsets(counts)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(d_in + d_out)
+    st = torch.cuda.current_stream().cuda_stream
+    y = torch.full((R, d_out + 8), -77.0, device="cuda")
+    if dtype == "i8":
+        d_in = d_in // 16 * 16
+        x, w = (torch.randint(-127, 128, s, generator=gen, device="cuda", dtype=torch.int32).to(torch.int8)
+                for s in ((R, d_in), (E, d_out, d_in)))
+        xs, ws = torch.rand(R, generator=gen, device="cuda") + 0.5, torch.rand((E, d_out), generator=gen, device="cuda") + 0.5
+        B.moe_i8_grouped_gemm(B.moe_grouped_t(R, E, d_in, d_out, B.MOE_DTYPE_I8, 2, 0, off.data_ptr(), d_in, d_out + 8),
+                              x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), y.data_ptr(), st)
+    else:
+        x = torch.randn((R, d_in), generator=gen, device="cuda").to(T[dtype])
+        w = (torch.randn((E, d_out, d_in), generator=gen, device="cuda") * 0.05).to(T[dtype])
+        B.moe_grouped_gemm(B.moe_grouped_t(R, E, d_in, d_out, MOE[dtype], 2, 0, off.data_ptr(), d_in, d_out + 8),
+                           x.data_ptr(), w.data_ptr(), y.data_ptr(), st)
+    _done()
+    assert bool((y[:, d_out:] == -77.0).all())
+    for e, (a, b) in enumerate(zip(off.tolist()[:-1], off.tolist()[1:])):
+        xe, we = x[a:b].double(), w[e].double()
+        ref = xe @ we.T
+        if dtype == "i8":
+            ref = ref * xs[a:b, None].double() * ws[e].double()
+            tol = ref.abs() * (4.5 * 2.0 ** -24)
+        else:
+            tol = (d_in / 16 + 13) * 2.0 ** -23 * (xe.abs() @ we.abs().T) + ref.abs() * 2.0 ** -24
+        assert bool(((y[a:b, :d_out].double() - ref).abs() <= tol).all()), f"expert {e}"
