@@ -447,8 +447,10 @@ typedef struct moe_grouped {
  * w [E][d_out][d_in], y [rows][d_out].  Sums in fp32, rounded once.  An F32
  * result is within about 1e-6 of the sum of its terms' absolute values: the tensor
  * cores' sums, which are cut and not rounded, are added up in short segments (over
- * millions of terms the roundings of that addition reach 3e-6).  Every row's result depends on its
- * own x and its expert's weights alone. */
+ * millions of terms the roundings of that addition reach 3e-6).  No other row's
+ * values and no other expert's weights reach a row's result; how its sum is split,
+ * and with that its last bits, depends on the sizes of the call, its number of rows
+ * among them. */
 moe_status_t moe_grouped_gemm(const moe_grouped_t* g, const void* x, const void* w, void* y,
                               void* stream);
 
@@ -475,7 +477,8 @@ moe_status_t moe_i8_quantize(int64_t rows, int32_t cols, int32_t dtype, const vo
 
 /* The grouped product of 8-bit codes: y[r][n] = x_scale[r] w_scale[e][n] *
  * sum_k xq[r][k] wq[e][n][k], the sum exact in int32; xq [rows][d_in],
- * x_scale [rows], wq [E][d_out][d_in], w_scale [E][d_out]. */
+ * x_scale [rows], wq [E][d_out][d_in], w_scale [E][d_out].  The scales multiply the
+ * sum in fp32, x_scale first. */
 moe_status_t moe_i8_grouped_gemm(const moe_grouped_t* g, const void* xq, const float* x_scale,
                                  const void* wq, const float* w_scale, void* y, void* stream);
 
@@ -500,9 +503,9 @@ moe_status_t moe_swiglu_i8(int64_t rows, int32_t cols, int32_t dtype, const void
                            void* stream);
 
 /* Read and clear the sticky error word of the experts' operators on the
- * current device (synchronises the device): OK, DEVICE_FLAG (an offsets table
- * that was not sound; that call wrote nothing) or TIMEOUT (a bounded wait ran
- * out; that call's output is incomplete). */
+ * current device, one for all of its streams (synchronises the device): OK,
+ * DEVICE_FLAG (an offsets table that was not sound; that call wrote nothing) or
+ * TIMEOUT (a bounded wait ran out; that call's output is incomplete). */
 moe_status_t moe_grouped_status(void);
 
 /* Static description of a status code (never NULL).  No counterpart on the

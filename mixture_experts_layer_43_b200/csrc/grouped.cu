@@ -34,8 +34,9 @@
 // its way; now 138 K cycles for 131 K of MMA in a product of one expert).  On a
 // DeepSeek-shaped prompt (24576 rows, 64 experts of 2048 x 2816, Zipf loads) the
 // tensor pipe is active in 65% of the cycles and DRAM moves the algorithm's bytes
-// once (977 MB); over half a second of such calls the power cap, not the kernel,
-// sets the time (244 us in a short run, 285 us sustained).
+// once (977 MB): 250 us in a short run, and as long with equal loads.  Over seconds
+// the power cap lowers the clock to 1.27 GHz (of 1.965) and the time is 289 us, 980
+// TFLOP/s, where a dense product of large matrices keeps 1390 under the same cap.
 #include <atomic>
 #include <cmath>
 
@@ -67,8 +68,8 @@ constexpr int kStages = 6;
 // nearest.  Products of bf16 have 16 significant bits and mostly fit: 512 terms of
 // one sign lose 7e-7 of their sum.  Products of fp16 have up to 22, and the cut
 // terms add their share: 2.5e-6 in 512 terms, 1.1e-6 in 256, 4.6e-7 in 128.  The
-// shorter segments cost 3 to 12% (DeepSeek-shaped dgrad with an fp32 result 268 us
-// with 512, 275 with 256, 293 to 317 with 128).
+// shorter segments cost a tenth to a fifth: DeepSeek-shaped gemm and dgrad with fp32
+// results 277 and 262 us in bf16 (255 and 243 with 16-bit ones), 309 and 317 in fp16.
 constexpr int kSegment = 8, kSegmentF16 = 2;
 // A 16-bit result shows it only over long reductions: n terms of one sign in one
 // sum lose 4.8e-9 n of it in fp16 (measured, 2^17 to 2^22 terms: 2.1e-4 to 6.9e-3)
